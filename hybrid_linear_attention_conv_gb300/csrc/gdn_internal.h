@@ -168,6 +168,7 @@ int report_error(int code, const char* fmt, ...);
 int check_shape_arg(const gdn_shape* s, bool need_single);  // head sizes, Hv % Hk, grid limits
 int check_pointer(const void* p, const char* name);          // non-NULL and 16-byte aligned
 int device_sm_count();                                        // SMs of the current device (cached)
+uint64_t wait_limit_ns();                                     // gdn_set_wait_limit_ns's (gdn_prefill.cu)
 
 // Launchers (return the cudaError_t of the launch).
 // kda: a decay per key channel (alpha [.., Hv, dk]) instead of one per head.

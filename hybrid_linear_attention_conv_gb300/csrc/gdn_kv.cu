@@ -1,0 +1,579 @@
+// gdn_kv.cu -- the paged 8-bit key/value cache of the decoder's attention
+// layers: the host side of its entry points (validation and launches), the
+// plan kernel (pages, slots and row offsets from the requests' lengths) and
+// the append kernel (a step's k and v rows into e4m3 codes and scales).
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "gdn_kv.cuh"
+#include "gdn_tc.cuh"
+
+namespace gdn {
+namespace {
+
+// ---------------------------------------------------------------------------
+// plan
+//
+// start = exclusive prefix of the new tokens, off = exclusive prefix of the
+// pages wanted, over the requests; every table entry and slot then follows
+// from two binary searches.  Each CTA computes both prefixes for itself (two
+// reads of 12 bytes a request, out of the L2 but for the first) and writes its
+// share of the outputs, so nothing waits on another CTA.  A slot takes its page from
+// the table's old entries or straight from the free stack, never from the
+// entries this launch writes.
+// ---------------------------------------------------------------------------
+constexpr int kPlanThreads = 512;
+constexpr int kPlanMaxB = 12288;  // 2 x 4 bytes a request of shared memory
+
+__device__ __forceinline__ long long warp_scan_ll(long long v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(~0u, v, o);
+        if ((threadIdx.x & 31) >= o) v += u;
+    }
+    return v;
+}
+
+// Largest i in [0, n) with a[i] <= x, for ascending a with a[0] <= x.
+__device__ __forceinline__ int find_last(const int32_t* a, int n, int x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) gdn_kv_plan_kernel(KvPlanParams p) {
+    extern __shared__ int32_t plan_smem[];
+    int32_t* start = plan_smem;       // [B]
+    int32_t* off = plan_smem + p.B;   // [B]
+    __shared__ long long sums[2][kPlanThreads / 32];
+    __shared__ int bad;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int P = 1 << p.log2_page;
+    if (tid == 0) bad = 0;
+    __syncthreads();
+
+    const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
+    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+    long long rows = 0, need = 0;
+    int wrong = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int len = p.lens[b], add = p.add[b], held = p.held[b];
+        if (len < 0 || add < 0 || held < 0 || held > p.width) {
+            wrong |= 8;
+            continue;
+        }
+        const long long want = ((long long)len + add + P - 1) >> p.log2_page;
+        if (want > p.width) wrong |= 2;
+        rows += add;
+        need += want > held ? want - held : 0;
+    }
+    const long long in_rows = warp_scan_ll(rows), in_need = warp_scan_ll(need);
+    if (lane == 31) {
+        sums[0][warp] = in_rows;
+        sums[1][warp] = in_need;
+    }
+    if (wrong) atomicOr(&bad, wrong);
+    __syncthreads();
+    long long before_rows = in_rows - rows, before_need = in_need - need, all_rows = 0, all_need = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (w < warp) {
+            before_rows += sums[0][w];
+            before_need += sums[1][w];
+        }
+        all_rows += sums[0][w];
+        all_need += sums[1][w];
+    }
+    const int count = p.free_count[0];
+    int status = bad;
+    if (count < 0 || count > p.free_cap) status |= 8;
+    if (all_need > count) status |= 1;
+    if (all_rows > p.rows) status |= 4;
+    const bool ok = status == 0;
+
+    for (int b = b0; b < b1; ++b) {  // ok: every prefix fits 32 bits
+        const int len = p.lens[b], add = p.add[b], held = p.held[b];
+        int want = held;
+        if (ok) {
+            start[b] = (int)before_rows;
+            off[b] = (int)before_need;
+            want = max(held, (int)(((long long)len + add + P - 1) >> p.log2_page));
+        }
+        if (blockIdx.x == 0) {
+            p.start[b] = ok ? (int)before_rows : 0;
+            p.lens_out[b] = ok ? len + add : len;
+            p.held_out[b] = want;
+        }
+        before_rows += add;
+        before_need += want - held;
+    }
+    if (blockIdx.x == 0 && tid == 0) {
+        p.start[p.B] = ok ? (int)all_rows : 0;
+        p.free_count_out[0] = ok ? count - (int)all_need : count;
+        p.status[0] = status;
+    }
+    __syncthreads();
+
+    const int n_rows = ok ? (int)all_rows : 0, n_need = ok ? (int)all_need : 0;
+    const int first = blockIdx.x * kPlanThreads + tid, stride = gridDim.x * kPlanThreads;
+    for (int i = first; i < n_need; i += stride) {
+        const int b = find_last(off, p.B, i);
+        p.table[(int64_t)b * p.width + p.held[b] + (i - off[b])] = p.free_pages[count - 1 - i];
+    }
+    for (int r = first; r < p.rows; r += stride) {
+        int64_t slot = -1;
+        if (r < n_rows) {
+            const int b = find_last(start, p.B, r);
+            const int pos = p.lens[b] + r - start[b], j = pos >> p.log2_page, held = p.held[b];
+            const int page = j < held ? p.table[(int64_t)b * p.width + j] : p.free_pages[count - 1 - off[b] - (j - held)];
+            slot = ((int64_t)page << p.log2_page) + (pos & (P - 1));
+        }
+        p.slots[r] = slot;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// append
+//
+// A run is a stretch of rows with consecutive slots in one page.  Its block
+// (page, head) gets the scale 2^e: e the smallest with amax <= 448 * 2^e over
+// the run's finite values, or the block's old exponent where that is larger
+// and the page holds earlier tokens.  Scaling by a power of two is exact, so a
+// code is the e4m3 number nearest to the value, whatever else is in the block;
+// where the scale grows, the earlier rows' codes move by the same power, which
+// only rounds what falls below e4m3's smallest normal number.  (A scale of
+// amax / 448 would round every code twice, and re-round every code at each
+// growth; the power of two costs at most one bit of e4m3's 18 binades.)
+//
+// The work is one pass over bf16 rows (2 bytes in, 1 out), bound by memory
+// for prompts and by latency for single tokens.  A CTA looks at `tile` rows of
+// one head of k or v, finds the runs that begin there with a ballot, lets a
+// warp take each short run, and takes the long ones as a whole, a thread
+// holding its part of the run in registers between the maximum and the
+// conversion.
+// ---------------------------------------------------------------------------
+constexpr int kAppendThreads = 256;
+constexpr int kAppendWarps = kAppendThreads / 32;
+constexpr int kAppendShort = 4;  // rows that one warp takes
+
+__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
+
+// 8 bf16 (packed) times f to 8 e4m3 codes; values that are not finite give 0.
+__device__ __forceinline__ uint2 codes8(uint4 x, float f, bool finite) {
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a = __uint_as_float(w[i] << 16), b = __uint_as_float(w[i] & 0xffff0000u);
+        if (!finite) {
+            a = isfinite(a) ? a : 0.0f;
+            b = isfinite(b) ? b : 0.0f;
+        }
+        c[i] = e4m3x2(a * f, b * f);
+    }
+    return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+// The largest finite |x| of 8 bf16, as bits, where some are not finite.
+__device__ __forceinline__ uint32_t max_finite8(uint32_t m, uint4 x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t a = w[i] & 0x7fffu, b = (w[i] >> 16) & 0x7fffu;
+        if (a < 0x7f80u) m = max(m, a);
+        if (b < 0x7f80u) m = max(m, b);
+    }
+    return m;
+}
+
+// 16 codes times 2^-k (k > 0), to nearest even.
+__device__ __forceinline__ uint32_t shrink4(uint32_t w, float f) {
+    const float2 a = float2_of_e4m3x2(w & 0xffffu), b = float2_of_e4m3x2(w >> 16);
+    return e4m3x2(a.x * f, a.y * f) | (e4m3x2(b.x * f, b.y * f) << 16);
+}
+
+// The run of n rows from row t, by `threads` threads of which this is `who`,
+// each holding up to CH chunks of 8 values; Max reduces a maximum over them.
+template <int CH, class Max>
+__device__ __forceinline__ void append_run(const KvAppendParams& p, int t, int n, int64_t slot, int head, bool is_v, int who,
+                                           int threads, Max&& reduce_max) {
+    const uint16_t* src = (is_v ? p.v : p.k) + (int64_t)head * p.d;
+    const int64_t ld = is_v ? p.ldv : p.ldk;
+    const int per_row = p.d >> 3, chunks = n * per_row, shift = p.d == 256 ? 5 : 4;
+    uint4 x[CH];
+    uint32_t m2 = 0, missing = 0;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int c = who + i * threads;
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (c < chunks) {
+            int row = t + (c >> shift);
+            if (p.rows != nullptr) row = p.rows[row];
+            if (row < 0 || row >= p.n_src) missing = 0x7f80u;  // a source row that is not there: the block's scale becomes NaN
+            else x[i] = *reinterpret_cast<const uint4*>(src + row * ld + (c & (per_row - 1)) * 8);
+        }
+        m2 = max_abs2(max_abs2(max_abs2(max_abs2(m2, x[i].x), x[i].y), x[i].z), x[i].w);
+    }
+    uint32_t top = reduce_max(max(max(m2 & 0xffffu, m2 >> 16), missing));
+    const bool finite = top < 0x7f80u;
+    if (!finite) {
+        uint32_t f = 0;
+#pragma unroll
+        for (int i = 0; i < CH; ++i) f = max_finite8(f, x[i]);
+        top = reduce_max(f);
+    }
+    const int64_t page = slot >> p.log2_page;
+    const int at = (int)(slot & ((1 << p.log2_page) - 1));
+    float* scale = (is_v ? p.v_scale : p.k_scale) + page * p.Hkv + head;
+    uint8_t* block = (is_v ? p.v_cache : p.k_cache) + ((page * p.Hkv + head) << p.log2_page) * p.d;
+    const float fresh = exp2_int(scale_exp_of_bf16(top));
+    const float old = at > 0 ? *scale : 0.0f;
+    reduce_max(0u);  // every thread has read the old scale before it is replaced
+    const bool poisoned = at > 0 && !(old > 0.0f && old < INFINITY);  // earlier rows that are not numbers stay so
+    const float now = poisoned ? fresh : fmaxf(old, fresh);
+    // the scales that this kernel writes are powers of two; one that is not
+    // (the caller's own) divides once, and its codes are re-rounded on growth
+    const float inv = 1.0f / now;
+    if (at > 0 && !poisoned && now > old) {
+        const float f = old * inv;
+        for (int c = who; c < (at * p.d) >> 4; c += threads) {
+            uint4* q = reinterpret_cast<uint4*>(block) + c;
+            const uint4 w = *q;
+            *q = make_uint4(shrink4(w.x, f), shrink4(w.y, f), shrink4(w.z, f), shrink4(w.w, f));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int c = who + i * threads;
+        if (c < chunks) *reinterpret_cast<uint2*>(block + (int64_t)at * p.d + (int64_t)c * 8) = codes8(x[i], inv, finite);
+    }
+    if (who == 0) *scale = finite && !poisoned ? now : __int_as_float(0x7fffffff);
+}
+
+template <int CH>
+__global__ void __launch_bounds__(kAppendThreads) gdn_kv_append_kernel(KvAppendParams p) {
+    __shared__ uint32_t warp_max[2][kAppendWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int head = blockIdx.y, t0 = blockIdx.x * p.tile, P = 1 << p.log2_page;
+    const bool is_v = blockIdx.z != 0;
+    const int64_t last_slot = (int64_t)p.pages << p.log2_page;
+
+    // Rows t0 .. t0 + tile - 1: a row begins a run unless it follows the row
+    // before it inside a page.  Every warp finds the same runs.
+    const int t = t0 + lane;
+    const bool mine = lane < p.tile && t < p.T;
+    const int64_t slot = mine ? p.slots[t] : -1;
+    const int64_t before = mine && t > 0 ? p.slots[t - 1] : -2;
+    const bool valid = slot >= 0 && slot < last_slot;
+    const bool begins = valid && (before != slot - 1 || (slot & (P - 1)) == 0);
+    uint32_t left = __ballot_sync(~0u, begins);
+    const uint32_t ends = ~__ballot_sync(~0u, valid && !begins);  // rows that do not continue a run
+    int phase = 0, nth = 0;
+    while (left) {  // uniform in the CTA
+        const int l = __ffs(left) - 1;
+        left &= left - 1;
+        const int64_t s0 = __shfl_sync(~0u, slot, l);
+        const int room = P - (int)(s0 & (P - 1));
+        const uint32_t after = l == 31 ? 0u : ends >> (l + 1);
+        int n = after ? __ffs(after) : 32 - l;  // a row past the tile does not continue in it
+        if (l + n >= p.tile) {  // up to the tile's end: the run may go on past it
+            n = p.tile - l;
+            while (n < room) {
+                const int u = t0 + l + n + lane;
+                const uint32_t stop = ~__ballot_sync(~0u, u < p.T && n + lane < room && p.slots[min(u, p.T - 1)] == s0 + n + lane);
+                if (stop) {
+                    n += __ffs(stop) - 1;
+                    break;
+                }
+                n += 32;
+            }
+        }
+        n = min(n, min(room, p.T - (t0 + l)));
+        if (n <= kAppendShort) {
+            if (nth++ % kAppendWarps == warp)
+                append_run<kAppendShort>(p, t0 + l, n, s0, head, is_v, lane, 32,
+                                         [](uint32_t m) { return __reduce_max_sync(~0u, m); });
+        } else {
+            append_run<CH>(p, t0 + l, n, s0, head, is_v, tid, kAppendThreads, [&](uint32_t m) {
+                m = __reduce_max_sync(~0u, m);
+                if (lane == 0) warp_max[phase][warp] = m;
+                __syncthreads();
+                uint32_t r = 0;
+#pragma unroll
+                for (int w = 0; w < kAppendWarps; ++w) r = max(r, warp_max[phase][w]);
+                phase ^= 1;  // the next use writes the other half; the one after it lies behind a barrier
+                return r;
+            });
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// validation
+// ---------------------------------------------------------------------------
+int check_kv_shape(const gdn_kv_shape* s) {
+    if (s == nullptr) return report_error(GDN_ERR_INVALID_ARG, "shape is NULL");
+    if (s->B < 0 || s->Hq < 1 || s->Hkv < 1 || s->pages < 0 || s->width < 0)
+        return report_error(GDN_ERR_UNSUPPORTED_SHAPE, "bad sizes: B=%d Hq=%d Hkv=%d pages=%d width=%d", s->B, s->Hq,
+                            s->Hkv, s->pages, s->width);
+    if (s->Hq % s->Hkv != 0)
+        return report_error(GDN_ERR_UNSUPPORTED_SHAPE, "Hq=%d is not a multiple of Hkv=%d", s->Hq, s->Hkv);
+    if (s->Hq > 1024) return report_error(GDN_ERR_UNSUPPORTED_SHAPE, "Hq=%d above 1024", s->Hq);
+    if (s->d != 128 && s->d != 256)
+        return report_error(GDN_ERR_UNSUPPORTED_SHAPE, "head size d=%d not in {128, 256}", s->d);
+    if (s->page != 32 && s->page != 64 && s->page != 128)
+        return report_error(GDN_ERR_UNSUPPORTED_SHAPE, "page=%d tokens not in {32, 64, 128}", s->page);
+    if ((int64_t)s->pages * s->Hkv * s->page > 0x7fffff00LL)
+        return report_error(GDN_ERR_UNSUPPORTED_SHAPE, "the cache has %lld rows, at most 2^31 - 256 are supported",
+                            (long long)s->pages * s->Hkv * s->page);
+    return GDN_OK;
+}
+
+int log2_of(int page) { return page == 32 ? 5 : page == 64 ? 6 : 7; }
+
+int check_row_stride(int64_t ld, int64_t row, const char* name) {
+    if (ld < row) return report_error(GDN_ERR_INVALID_ARG, "%s=%lld below a row's %lld elements", name, (long long)ld, (long long)row);
+    if (ld % 8 != 0) return report_error(GDN_ERR_MISALIGNED, "%s=%lld is not a multiple of 8 elements (16 bytes)", name, (long long)ld);
+    return GDN_OK;
+}
+
+// Rows a CTA looks at.  Few rows are mostly single tokens, a warp each; among
+// many rows most belong to long runs, and a CTA that finds none has only cost
+// its launch.
+int append_tile_rows(int T) { return T <= 1024 ? kAppendWarps : 32; }
+
+// cuTensorMapEncodeTiled from the driver, looked up once.
+PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+        (void)cudaGetLastError();
+    });
+    return fn;
+}
+
+// A cache as rows of d codes, loaded in boxes of 32 rows x 128 bytes with the
+// 128-byte swizzle (16-byte chunk c of row r lies at c ^ (r & 7)).
+bool encode_cache_map(CUtensorMap* map, const uint8_t* cache, const gdn_kv_shape* s) {
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = tmap_encoder();
+    if (enc == nullptr) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)s->d, (cuuint64_t)s->pages * s->Hkv * s->page};
+    const cuuint64_t strides[1] = {(cuuint64_t)s->d};
+    const cuuint32_t box[2] = {128, 32}, unit[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(cache), dims, strides, box, unit,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+cudaError_t launch_kv_plan(const KvPlanParams& p, cudaStream_t s) {
+    static std::once_flag once[64];
+    static cudaError_t err[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= 64) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+    std::call_once(once[dev], [dev] {
+        err[dev] = cudaFuncSetAttribute(gdn_kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanMaxB * 8);
+    });
+    if (err[dev] != cudaSuccess) return err[dev];
+    // a CTA for every two rows of its threads, up to one per SM
+    const int grid = std::max(1, std::min(device_sm_count(), (p.rows + 2 * kPlanThreads - 1) / (2 * kPlanThreads)));
+    gdn_kv_plan_kernel<<<grid, kPlanThreads, (size_t)p.B * 8, s>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv_append(const KvAppendParams& p0, cudaStream_t s) {
+    KvAppendParams p = p0;
+    p.tile = append_tile_rows(p.T);
+    const dim3 grid((unsigned)((p.T + p.tile - 1) / p.tile), (unsigned)p.Hkv, 2);
+    const int chunks = ((1 << p.log2_page) * p.d) / (8 * kAppendThreads);  // a whole page's, for each thread
+    switch (chunks) {
+        case 2: gdn_kv_append_kernel<2><<<grid, kAppendThreads, 0, s>>>(p); break;
+        case 4: gdn_kv_append_kernel<4><<<grid, kAppendThreads, 0, s>>>(p); break;
+        case 8: gdn_kv_append_kernel<8><<<grid, kAppendThreads, 0, s>>>(p); break;
+        default: gdn_kv_append_kernel<16><<<grid, kAppendThreads, 0, s>>>(p); break;
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+int gdn_kv_plan(const gdn_kv_shape* shape, const int32_t* lens, const int32_t* add, const int32_t* held,
+                const int32_t* free_pages, int32_t free_cap, const int32_t* free_count, int32_t* table, int32_t rows,
+                int32_t* lens_out, int32_t* held_out, int32_t* free_count_out, int32_t* start, int64_t* slots,
+                int32_t* status, void* stream) {
+    int rc;
+    if ((rc = check_kv_shape(shape)) != GDN_OK) return rc;
+    if (shape->B > kPlanMaxB)
+        return report_error(GDN_ERR_UNSUPPORTED_SHAPE, "B=%d requests, one plan takes at most %d", shape->B, kPlanMaxB);
+    if ((int64_t)shape->width * shape->page > 0x7fffffffLL)
+        return report_error(GDN_ERR_UNSUPPORTED_SHAPE, "width=%d pages of %d tokens exceed 2^31 - 1 tokens", shape->width, shape->page);
+    if (rows < 0 || free_cap < 0) return report_error(GDN_ERR_INVALID_ARG, "negative size rows=%d free_cap=%d", rows, free_cap);
+    const bool some = shape->B > 0;
+    if ((some && ((rc = check_pointer(lens, "lens")) || (rc = check_pointer(add, "add")) || (rc = check_pointer(held, "held")) ||
+                  (rc = check_pointer(lens_out, "lens_out")) || (rc = check_pointer(held_out, "held_out")))) ||
+        (some && shape->width > 0 && (rc = check_pointer(table, "table"))) ||
+        (free_cap > 0 && (rc = check_pointer(free_pages, "free_pages"))) || (rc = check_pointer(free_count, "free_count")) ||
+        (rc = check_pointer(free_count_out, "free_count_out")) || (rc = check_pointer(start, "start")) ||
+        (rows > 0 && (rc = check_pointer(slots, "slots"))) || (rc = check_pointer(status, "status")))
+        return rc;
+    // every CTA reads all of these while others write the outputs
+    const void* in[4] = {lens, add, held, free_count};
+    const void* out[3] = {lens_out, held_out, free_count_out};
+    for (const void* a : in)
+        for (const void* b : out)
+            if (a != nullptr && a == b) return report_error(GDN_ERR_INVALID_ARG, "an output is one of the inputs (they must be distinct buffers)");
+    KvPlanParams p{};
+    p.lens = lens;
+    p.add = add;
+    p.held = held;
+    p.free_pages = free_pages;
+    p.free_count = free_count;
+    p.table = table;
+    p.lens_out = lens_out;
+    p.held_out = held_out;
+    p.free_count_out = free_count_out;
+    p.start = start;
+    p.slots = slots;
+    p.status = status;
+    p.B = shape->B;
+    p.width = shape->width;
+    p.log2_page = log2_of(shape->page);
+    p.free_cap = free_cap;
+    p.rows = rows;
+    cudaError_t e = launch_kv_plan(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GDN_OK : cuda_error(e, "cache plan launch");
+}
+
+int gdn_kv_append(const gdn_kv_shape* shape, int32_t T, const gdn_bf16* k, int64_t ldk, const gdn_bf16* v, int64_t ldv,
+                  int32_t n_src, const int64_t* slots, const int32_t* rows, uint8_t* k_cache, uint8_t* v_cache,
+                  float* k_scale, float* v_scale, void* stream) {
+    int rc;
+    if ((rc = check_kv_shape(shape)) != GDN_OK) return rc;
+    if (T < 0 || n_src < 0) return report_error(GDN_ERR_INVALID_ARG, "negative size T=%d n_src=%d", T, n_src);
+    if (shape->Hkv > 65535) return report_error(GDN_ERR_UNSUPPORTED_SHAPE, "Hkv=%d exceeds the grid limit 65535", shape->Hkv);
+    const int64_t row = (int64_t)shape->Hkv * shape->d;
+    if ((rc = check_row_stride(ldk, row, "ldk")) || (rc = check_row_stride(ldv, row, "ldv"))) return rc;
+    if (rows == nullptr && n_src < T)
+        return report_error(GDN_ERR_INVALID_ARG, "k and v have %d rows, T=%d are to be appended", n_src, T);
+    if (T == 0 || shape->pages == 0) return GDN_OK;  // nothing to do; pointers may be NULL
+    if ((rc = check_pointer(slots, "slots")) || (rc = check_pointer(k_cache, "k_cache")) ||
+        (rc = check_pointer(v_cache, "v_cache")) || (rc = check_pointer(k_scale, "k_scale")) ||
+        (rc = check_pointer(v_scale, "v_scale")))
+        return rc;
+    if (n_src > 0 && ((rc = check_pointer(k, "k")) || (rc = check_pointer(v, "v")))) return rc;
+    if (rows != nullptr && (rc = check_pointer(rows, "rows")) != GDN_OK) return rc;
+    KvAppendParams p{};
+    p.k = k;
+    p.v = v;
+    p.slots = slots;
+    p.rows = rows;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.ldk = ldk;
+    p.ldv = ldv;
+    p.T = T;
+    p.n_src = n_src;
+    p.Hkv = shape->Hkv;
+    p.d = shape->d;
+    p.log2_page = log2_of(shape->page);
+    p.pages = shape->pages;
+    cudaError_t e = launch_kv_append(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GDN_OK : cuda_error(e, "cache append launch");
+}
+
+size_t gdn_kv_attention_workspace_bytes(const gdn_kv_shape* shape) {
+    if (check_kv_shape(shape) != GDN_OK) return 0;
+    return kKvPartialsAt + kv_attn_rows_workspace(shape->d);
+}
+
+int gdn_kv_attention(const gdn_kv_shape* shape, int32_t T, const gdn_bf16* q, int64_t ldq, const uint8_t* k_cache,
+                     const uint8_t* v_cache, const float* k_scale, const float* v_scale, const int32_t* table,
+                     const int32_t* start, const int32_t* lens, const int64_t* tree, float scale, gdn_bf16* out,
+                     float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc;
+    if ((rc = check_kv_shape(shape)) != GDN_OK) return rc;
+    if (T < 0) return report_error(GDN_ERR_INVALID_ARG, "T=%d < 0", T);
+    if ((int64_t)T * (shape->Hq / shape->Hkv) > 0x7fffffffLL || (int64_t)shape->width * shape->page > 0x7fffffffLL)
+        return report_error(GDN_ERR_UNSUPPORTED_SHAPE, "T=%d rows or width=%d pages exceed 2^31 - 1 rows or tokens", T, shape->width);
+    if ((rc = check_row_stride(ldq, (int64_t)shape->Hq * shape->d, "ldq")) != GDN_OK) return rc;
+    if (!(scale > 0.0f) || scale > 1e6f) return report_error(GDN_ERR_INVALID_ARG, "scale=%g outside (0, 1e6]", (double)scale);
+    if (T == 0 || shape->B == 0) return GDN_OK;  // nothing to do; pointers may be NULL
+    if (shape->pages < 1 || shape->width < 1)
+        return report_error(GDN_ERR_UNSUPPORTED_SHAPE, "pages=%d width=%d: there is no cache to read", shape->pages, shape->width);
+    if ((rc = check_pointer(q, "q")) || (rc = check_pointer(k_cache, "k_cache")) || (rc = check_pointer(v_cache, "v_cache")) ||
+        (rc = check_pointer(k_scale, "k_scale")) || (rc = check_pointer(v_scale, "v_scale")) ||
+        (rc = check_pointer(table, "table")) || (rc = check_pointer(start, "start")) || (rc = check_pointer(lens, "lens")) ||
+        (rc = check_pointer(out, "out")))
+        return rc;
+    if (tree != nullptr && (rc = check_pointer(tree, "tree")) != GDN_OK) return rc;
+    if (lse != nullptr && (rc = check_pointer(lse, "lse")) != GDN_OK) return rc;
+    if (workspace == nullptr) return report_error(GDN_ERR_WORKSPACE, "workspace is NULL");
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return report_error(GDN_ERR_MISALIGNED, "workspace (%p) is not 256-byte aligned", workspace);
+    const size_t need = gdn_kv_attention_workspace_bytes(shape);
+    if (workspace_bytes < need)
+        return report_error(GDN_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+    KvAttnParams p{};
+    if (!encode_cache_map(&p.tm_k, k_cache, shape) || !encode_cache_map(&p.tm_v, v_cache, shape))
+        return report_error(GDN_ERR_CUDA, "the driver refused the cache's tensor maps");
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.q = q;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.table = table;
+    p.start = start;
+    p.lens = lens;
+    p.tree = tree;
+    p.out = out;
+    p.lse = lse;
+    p.status = reinterpret_cast<int*>(ws);
+    p.counters = reinterpret_cast<unsigned*>(ws + 256);
+    p.partials = reinterpret_cast<float*>(ws + kKvPartialsAt);
+    p.wait_ns = wait_limit_ns();
+    p.ldq = ldq;
+    p.T = T;
+    p.B = shape->B;
+    p.Hq = shape->Hq;
+    p.Hkv = shape->Hkv;
+    p.G = shape->Hq / shape->Hkv;
+    p.width = shape->width;
+    p.pages = shape->pages;
+    p.log2_page = log2_of(shape->page);
+    p.scale_log2 = scale * 1.4426950408889634f;
+    cudaError_t e = launch_kv_attn_rows(p, shape->d, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GDN_OK : cuda_error(e, "cache attention launch");
+}
+
+int gdn_kv_attention_status(const void* workspace, void* stream, int32_t* status) {
+    if (workspace == nullptr) return report_error(GDN_ERR_WORKSPACE, "workspace is NULL");
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int32_t word = 0;
+    cudaError_t e = cudaMemcpyAsync(&word, workspace, sizeof word, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e != cudaSuccess) return cuda_error(e, "reading the attention's status word");
+    if (status != nullptr) *status = word;
+    if (word != 0) return report_error(GDN_ERR_TIMEOUT, "a bounded device wait of an attention call gave up (status %d)", word);
+    return GDN_OK;
+}
+
+}  // extern "C"

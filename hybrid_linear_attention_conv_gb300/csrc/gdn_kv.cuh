@@ -1,0 +1,140 @@
+// gdn_kv.cuh -- what the paged 8-bit cache's kernels share: the launch
+// parameters that gdn_kv.cu fills after validation, the power-of-two scales,
+// and the split of a value into two e4m3 numbers.  Nothing here is part of
+// the ABI.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gdn_internal.h"
+
+namespace gdn {
+
+// A block's scale is 2^e.  e4m3's largest number is 448 = 1.75 * 2^8.
+constexpr int kScaleMinExp = -100, kScaleMaxExp = 120;
+
+// Smallest e with amax <= 448 * 2^e, clamped, for the finite bf16 with these
+// bits (sign cleared).  amax = m * 2^E: e = E - 8 while m <= 1.75.
+__host__ __device__ inline int scale_exp_of_bf16(uint32_t bits) {
+    const int E = (int)(bits >> 7) - 127;
+    const int e = E - 8 + ((bits & 0x7f) > 0x60 ? 1 : 0);
+    return e < kScaleMinExp ? kScaleMinExp : e > kScaleMaxExp ? kScaleMaxExp : e;
+}
+
+// Row coordinate of tokens [pos, pos + 32) of a sequence in the cache seen as
+// rows of d codes: rows of a page's head are adjacent.  A page that the table
+// does not have (outside the table's width or the cache) gives `rows`, one
+// past the last row, which the copy engine fills with zeros.
+__host__ __device__ inline int32_t cache_row(int32_t page, int32_t pages, int32_t Hkv, int32_t h, int32_t log2_page,
+                                             int32_t pos) {
+    if (page < 0 || page >= pages) return (int32_t)((int64_t)pages * Hkv << log2_page);
+    return (int32_t)((((int64_t)page * Hkv + h) << log2_page) + (pos & ((1 << log2_page) - 1)));
+}
+
+struct KvPlanParams {
+    const int32_t* lens;        // [B] tokens cached
+    const int32_t* add;         // [B] tokens to come
+    const int32_t* held;        // [B] pages held
+    const int32_t* free_pages;  // [free_cap] a stack: the next page is the last
+    const int32_t* free_count;  // [1]
+    int32_t* table;             // [B, width]
+    int32_t* lens_out;
+    int32_t* held_out;
+    int32_t* free_count_out;
+    int32_t* start;             // [B + 1]
+    int64_t* slots;             // [rows]
+    int32_t* status;            // [1]
+    int B, width, log2_page, free_cap, rows;
+};
+
+struct KvAppendParams {
+    const uint16_t* k;          // bf16 rows [n_src, Hkv, d], row stride ldk
+    const uint16_t* v;
+    const int64_t* slots;       // [T]
+    const int32_t* rows;        // [T] source rows, or nullptr (row t)
+    uint8_t* k_cache;           // [pages, Hkv, P, d]
+    uint8_t* v_cache;
+    float* k_scale;             // [pages, Hkv]
+    float* v_scale;
+    int64_t ldk, ldv;
+    int T, n_src, Hkv, d, log2_page, pages;
+    int tile;                   // rows that a CTA looks at for the beginnings of runs
+};
+
+struct KvAttnParams {
+    CUtensorMap tm_k, tm_v;     // the caches as [pages * Hkv * P, d] bytes, 128-byte wide boxes
+    const uint16_t* q;          // bf16 rows [T, Hq, d], row stride ldq
+    const float* k_scale;       // [pages, Hkv]
+    const float* v_scale;
+    const int32_t* table;       // [B, width]
+    const int32_t* start;       // [B + 1]
+    const int32_t* lens;        // [B]
+    const int64_t* tree;        // [T] or nullptr
+    uint16_t* out;              // bf16 [T, Hq, d]
+    float* lse;                 // [T, Hq] or nullptr
+    int* status;                // workspace: the status word,
+    unsigned* counters;         // a counter for each CTA (zero between calls),
+    float* partials;            // and the partial results
+    uint64_t wait_ns;
+    int64_t ldq;
+    int T, B, Hq, Hkv, G, width, pages, log2_page;
+    float scale_log2;           // scale * log2(e)
+};
+
+// Workspace: 256 bytes of status, the counters, then the partial results.
+constexpr int kKvMaxCtas = 1024;
+constexpr size_t kKvPartialsAt = 256 + (size_t)kKvMaxCtas * 4;
+
+cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t s);
+cudaError_t launch_kv_plan(const KvPlanParams& p, cudaStream_t s);
+// One to eight query rows of a key/value head at a time (mma.sync).
+cudaError_t launch_kv_attn_rows(KvAttnParams& p, int d, cudaStream_t s);
+size_t kv_attn_rows_workspace(int d);
+
+#ifdef __CUDACC__
+// 2^e for e in the normal range.
+__device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
+
+// Two e4m3 codes (a in the low byte), to nearest even, saturating; NaN stays NaN.
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+    return r;
+}
+// The two e4m3 codes in the low half of w, as f16 (exact).
+__device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t w) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)w));
+    return r;
+}
+__device__ __forceinline__ float2 float2_of_e4m3x2(uint32_t w) {
+    const uint32_t h = f16x2_of_e4m3x2(w);
+    float2 r;
+    asm("{\n\t.reg .f16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "r"(h));
+    return r;
+}
+
+// Four values as e4m3 hi + lo: hi = RNE(x), lo = RNE(x - hi).  x - hi is exact
+// in fp32; hi + lo holds eight significant bits of |x| >= 2^-2 and is within
+// 2^-10 of smaller ones (lo's smallest step is 2^-9).  So a bf16 value is held
+// exactly while it is within 2^-10 of its row's largest.
+__device__ __forceinline__ void split4_e4m3(const float (&x)[4], uint32_t& hi, uint32_t& lo) {
+    const uint32_t h0 = e4m3x2(x[0], x[1]), h1 = e4m3x2(x[2], x[3]);
+    const float2 f0 = float2_of_e4m3x2(h0), f1 = float2_of_e4m3x2(h1);
+    const uint32_t l0 = e4m3x2(x[0] - f0.x, x[1] - f0.y), l1 = e4m3x2(x[2] - f1.x, x[3] - f1.y);
+    hi = h0 | (h1 << 16);
+    lo = l0 | (l1 << 16);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+#endif
+
+}  // namespace gdn

@@ -1513,6 +1513,10 @@ int read_status_word(const void* word, void* stream, int32_t* status) {
 }
 }  // namespace
 
+namespace gdn {
+uint64_t wait_limit_ns() { return g_wait_ns.load(); }
+}  // namespace gdn
+
 extern "C" {
 
 uint64_t gdn_set_wait_limit_ns(uint64_t ns) {

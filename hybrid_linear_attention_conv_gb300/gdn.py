@@ -73,6 +73,11 @@ EXPORTS = [
     "gdn_snapshot_signature",
     "gdn_snapshot_save",
     "gdn_snapshot_restore",
+    "gdn_kv_plan",
+    "gdn_kv_append",
+    "gdn_kv_attention_workspace_bytes",
+    "gdn_kv_attention",
+    "gdn_kv_attention_status",
 ]
 
 
@@ -85,6 +90,11 @@ class GdnError(RuntimeError):
 class gdn_shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("Hk", ctypes.c_int32), ("Hv", ctypes.c_int32),
                 ("dk", ctypes.c_int32), ("dv", ctypes.c_int32)]
+
+
+class gdn_kv_shape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("pages", ctypes.c_int32), ("width", ctypes.c_int32)]
 
 
 _lock = threading.Lock()
@@ -105,6 +115,7 @@ def load(path: str = LIB_PATH):
                               ctypes.c_size_t)
         I64 = ctypes.c_int64
         SH = ctypes.POINTER(gdn_shape)
+        KV = ctypes.POINTER(gdn_kv_shape)
         sig = {
             "gdn_abi_version": (ctypes.c_int, []),
             "gdn_last_error": (ctypes.c_char_p, []),
@@ -139,6 +150,11 @@ def load(path: str = LIB_PATH):
             "gdn_snapshot_signature": (ctypes.c_uint64, [SH, I32]),
             "gdn_snapshot_save": (ctypes.c_int, [SH, I32, I32, P, I64, P, I64, P, SZ, P, SZ, P]),
             "gdn_snapshot_restore": (ctypes.c_int, [SH, I32, I32, P, SZ, P, I64, P, I64, P, SZ, P]),
+            "gdn_kv_plan": (ctypes.c_int, [KV, P, P, P, P, I32, P, P, I32, P, P, P, P, P, P, P]),
+            "gdn_kv_append": (ctypes.c_int, [KV, I32, P, I64, P, I64, I32, P, P, P, P, P, P, P]),
+            "gdn_kv_attention_workspace_bytes": (SZ, [KV]),
+            "gdn_kv_attention": (ctypes.c_int, [KV, I32, P, I64, P, P, P, P, P, P, P, P, F, P, P, P, SZ, P]),
+            "gdn_kv_attention_status": (ctypes.c_int, [P, P, ctypes.POINTER(I32)]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -732,6 +748,124 @@ def read_snapshot_file(path: str, pinned: bool = True) -> torch.Tensor:
     """Read a blob file into (pinned) host memory, ready for snapshot_restore."""
     t = torch.from_numpy(np.fromfile(path, dtype=np.uint8))
     return t.pin_memory() if pinned else t
+
+
+# ---------------------------------------------------------------------------
+# the attention layers' paged 8-bit key/value cache
+# ---------------------------------------------------------------------------
+KV_PLAN_STATUS = {1: "the free pages do not suffice", 2: "a request outgrows its row of the block table",
+                  4: "more new tokens than rows", 8: "a negative or inconsistent count"}
+
+
+def _rows3(t: torch.Tensor, name: str, heads=None, d=None) -> tuple[ctypes.c_void_p, int]:
+    """A bf16 CUDA tensor [rows, heads, d] whose rows may be strided apart but are
+    each contiguous: (pointer, row stride in elements)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or (heads is not None and tuple(t.shape[1:]) != (heads, d)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (rows, {heads or 'heads'}, {d or 'd'})")
+    if (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"each row of {name} must be contiguous")
+    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return ctypes.c_void_p(t.data_ptr()), int(ld)
+
+
+def _kv_cache(k_cache, v_cache, k_scale, v_scale):
+    """Pointers of a cache: codes float8_e4m3fn [pages,Hkv,page,d], scales fp32 [pages,Hkv]."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be a tensor [pages, Hkv, page, d]")
+    shape = tuple(k_cache.shape)
+    return (_dev(k_cache, torch.float8_e4m3fn, "k_cache"), _dev(v_cache, torch.float8_e4m3fn, "v_cache", shape),
+            _dev(k_scale, torch.float32, "k_scale", shape[:2]), _dev(v_scale, torch.float32, "v_scale", shape[:2]))
+
+
+def kv_plan(lens, new, held, free_pages, free_count, table, page, rows, out=None):
+    """Pages, slots and row offsets of a step.  lens/new/held int32 [B], free_pages int32
+    [cap], free_count int32 [1], table int32 [B,width] (new entries written in place), page
+    tokens a page, rows: the step's tokens (or more).  Returns (lens, held, free_count, start
+    [B+1], slots int64 [rows], status [1]), or fills the tuple `out`; kv_plan_check reads status."""
+    B, width = table.shape
+    i32 = torch.int32
+    if out is None:
+        e = lambda n, dt=i32: torch.empty(n, dtype=dt, device=table.device)  # noqa: E731
+        out = (e(B), e(B), e(1), e(B + 1), e(rows, torch.int64), e(1))
+    shapes = ((B,), (B,), (1,), (B + 1,), (rows,), (1,))
+    names = ("lens_out", "held_out", "free_count_out", "start", "slots", "status")
+    ptrs = [_dev(t, torch.int64 if n == "slots" else i32, n, sh) for t, n, sh in zip(out, names, shapes)]
+    sh = gdn_kv_shape(B, 1, 1, 128, int(page), 0, width)
+    rc = load().gdn_kv_plan(ctypes.byref(sh), _dev(lens, i32, "lens", (B,)), _dev(new, i32, "new", (B,)),
+                            _dev(held, i32, "held", (B,)), _dev(free_pages, i32, "free_pages"), free_pages.numel(),
+                            _dev(free_count, i32, "free_count", (1,)), _dev(table, i32, "table"), int(rows), *ptrs, _stream())
+    _check(rc, "gdn_kv_plan")
+    return out
+
+
+def kv_plan_check(status: torch.Tensor) -> None:
+    """Synchronise and raise GdnError if the plan that wrote `status` handed nothing out."""
+    word = int(status.item())
+    if word:
+        raise GdnError(-100 - word, "gdn_kv_plan", "; ".join(m for bit, m in KV_PLAN_STATUS.items() if word & bit))
+
+
+def kv_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, rows=None) -> None:
+    """k, v bf16 [n,Hkv,d] (rows may be strided) into slots int64 [T] of the cache, in place:
+    codes float8_e4m3fn [pages,Hkv,page,d], scales fp32 [pages,Hkv].  rows int32 [T]: slot t
+    takes source row rows[t]."""
+    cache = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    pages, Hkv, page, d = k_cache.shape
+    T = slots.numel()
+    kp, ldk = _rows3(k, "k", Hkv, d)
+    vp, ldv = _rows3(v, "v", Hkv, d)
+    if k.shape[0] != v.shape[0]:
+        raise ValueError(f"k has {k.shape[0]} rows, v has {v.shape[0]}")
+    sh = gdn_kv_shape(1, Hkv, Hkv, d, page, pages, 0)
+    rc = load().gdn_kv_append(ctypes.byref(sh), T, kp, ldk, vp, ldv, k.shape[0], _dev(slots, torch.int64, "slots", (T,)),
+                              _dev(rows, torch.int32, "rows", (T,)), *cache, _stream())
+    _check(rc, "gdn_kv_append")
+
+
+def kv_attention_workspace_bytes(Hq, Hkv, d) -> int:
+    return int(load().gdn_kv_attention_workspace_bytes(ctypes.byref(gdn_kv_shape(1, int(Hq), int(Hkv), int(d), 32, 1, 1))))
+
+
+def kv_attention(q, k_cache, v_cache, k_scale, v_scale, table, start, lens, scale=None, tree=None, out=None, lse=None,
+                 workspace=None) -> torch.Tensor:
+    """q bf16 [T,Hq,d] (rows may be strided) over the cache -> out bf16 [T,Hq,d].  table int32
+    [B,width], start int32 [B+1] and lens int32 [B] as kv_plan leaves them; scale defaults to
+    d^-0.5; tree int64 [T]: the draft nodes that a query sees, as bits (causal without it);
+    lse fp32 [T,Hq], filled if given; workspace uint8, zeroed before its first use (by default
+    a new one)."""
+    cache = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    pages, Hkv, page, d = k_cache.shape
+    qp, ldq = _rows3(q, "q")
+    T, Hq = q.shape[0], q.shape[1]
+    if q.shape[2] != d:
+        raise ValueError(f"q has heads of {q.shape[2]}, the cache of {d}")
+    B, width = table.shape
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=q.device)
+    sh = gdn_kv_shape(B, Hq, Hkv, d, page, pages, width)
+    if workspace is None:
+        workspace = torch.zeros(max(int(load().gdn_kv_attention_workspace_bytes(ctypes.byref(sh))), 1), dtype=torch.uint8, device=q.device)
+    rc = load().gdn_kv_attention(ctypes.byref(sh), T, qp, ldq, *cache, _dev(table, torch.int32, "table"),
+                                 _dev(start, torch.int32, "start", (B + 1,)), _dev(lens, torch.int32, "lens", (B,)),
+                                 _dev(tree, torch.int64, "tree", (T,)), float(d ** -0.5 if scale is None else scale),
+                                 _dev(out, torch.bfloat16, "out", (T, Hq, d)), _dev(lse, torch.float32, "lse", (T, Hq)),
+                                 _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream())
+    _check(rc, "gdn_kv_attention")
+    return out
+
+
+def kv_attention_status(workspace: torch.Tensor) -> int:
+    """Synchronise the current stream and return the status word of the attention calls that
+    used `workspace` (0: their results are valid; non-zero: a bounded device wait gave up)."""
+    st = ctypes.c_int32(0)
+    rc = load().gdn_kv_attention_status(_dev(workspace, torch.uint8, "workspace"), _stream(), ctypes.byref(st))
+    if rc not in (0, -8):
+        _check(rc, "gdn_kv_attention_status")
+    return int(st.value)
 
 
 # ---------------------------------------------------------------------------

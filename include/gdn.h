@@ -634,6 +634,126 @@ int gdn_snapshot_restore(const gdn_shape* shape, int32_t layers, int32_t seq, co
                          int64_t tail_layer_stride, void* workspace, size_t workspace_bytes,
                          void* stream);
 
+/*
+ * ---- The attention layers' key/value cache, held in 8 bits -----------------
+ * The decoder's other layers attend over all earlier tokens, whose keys and
+ * values grow with the context ("Architecture" v0.14.2 section 8.1, table of
+ * layer kinds).  These calls keep them in pages of `page` tokens: codes in
+ * e4m3 (8-bit floating point, 4 exponent and 3 mantissa bits, largest number 448) and one fp32
+ * scale for each block, a page's tokens of one key/value head:
+ *   k_cache, v_cache  uint8 [pages, Hkv, page, d]   codes,
+ *   k_scale, v_scale  fp32 [pages, Hkv]             value = code * scale.
+ * A request's tokens lie, in order, in the pages of its row of the block
+ * table, table int32 [B, width].  A step is gdn_kv_plan (once), then
+ * gdn_kv_append and gdn_kv_attention for each layer.
+ * Shapes: d in {128, 256}; page in {32, 64, 128}; Hq a multiple of Hkv;
+ * pages * Hkv * page < 2^31 - 256.  Query head h reads key/value head
+ * h / (Hq / Hkv).  Slots: token position p of a request lies in slot
+ * table[b][p / page] * page + p % page.
+ */
+typedef struct gdn_kv_shape {
+    int32_t B;     /* requests */
+    int32_t Hq;    /* query heads */
+    int32_t Hkv;   /* key/value heads */
+    int32_t d;     /* head size */
+    int32_t page;  /* tokens of a page */
+    int32_t pages; /* pages of the cache */
+    int32_t width; /* entries of a block table's row */
+} gdn_kv_shape;
+
+/*
+ * gdn_kv_plan -- pages and slots for a step's new tokens, on the device, from
+ * the requests' lengths: request b goes from lens[b] to lens[b] + add[b]
+ * tokens.  Pages come off the end of the free stack, in the order of the
+ * requests; a request that already holds enough (its length was taken back,
+ * say) keeps what it holds.
+ *   lens, add, held  int32 [B]: tokens cached, tokens to come, pages held
+ *                    (held[b] <= width; the first held[b] table entries).
+ *   free_pages       int32 [free_cap], free_count int32 [1]: the stack of free
+ *                    pages, free_pages[0 .. free_count - 1].
+ *   table            int32 [B, width] in/out: new pages' entries are written.
+ *   rows             capacity of slots: the step's tokens, or more.
+ *   lens_out, held_out int32 [B], free_count_out int32 [1]: the state after the
+ *                    step; distinct buffers from lens, held and free_count.
+ *   start            int32 [B + 1]: request b's new tokens are rows start[b] ..
+ *                    start[b + 1] - 1 of the step.
+ *   slots            int64 [rows]: the rows' slots; -1 past the last row.
+ *   status           int32 [1]: 0, or bits of what is wrong: 1 the free pages do not
+ *                    suffice, 2 a request outgrows its table row, 4 more new
+ *                    tokens than rows, 8 a negative or inconsistent count.
+ *                    Nothing is handed out then: the state comes out as it went
+ *                    in, start is all 0 and slots all -1, so that the step's
+ *                    later calls do nothing.
+ * B <= 12288; Hq, Hkv and d of the shape are checked and not used.  Repeating
+ * a call with the same inputs repeats its outputs.
+ */
+int gdn_kv_plan(const gdn_kv_shape* shape, const int32_t* lens, const int32_t* add, const int32_t* held,
+                const int32_t* free_pages, int32_t free_cap, const int32_t* free_count, int32_t* table, int32_t rows,
+                int32_t* lens_out, int32_t* held_out, int32_t* free_count_out, int32_t* start, int64_t* slots,
+                int32_t* status, void* stream);
+
+/*
+ * gdn_kv_append -- T rows of keys and values into their slots.
+ *   k, v    bf16 [n_src, Hkv, d] with ldk, ldv elements between rows (slices of
+ *           a projection's rows; multiples of 8).
+ *   slots   int64 [T]; a row whose slot is negative or past the cache is left out.
+ *   rows    int32 [T], or NULL: slot t takes source row rows[t] (a draft tree's
+ *           accepted path, say) instead of row t.  A row outside [0, n_src)
+ *           counts as a value that is not finite.
+ * Rows with consecutive slots in one page are a run.  A block that a run begins
+ * (slot % page == 0) gets the scale 2^e, e the smallest with
+ * amax <= 448 * 2^e over the run's |k| (e in [-100, 120]); a block with earlier
+ * tokens keeps its scale or grows to that, and its earlier codes are re-rounded
+ * to the new scale.  Each code is the e4m3 number nearest to value / scale, to
+ * even.  A run with a value that is not finite makes its block's scale NaN (the
+ * block reads as NaN until it is begun again); codes are always finite.
+ * A page may take part in one run of a call only (as gdn_kv_plan's slots do).
+ */
+int gdn_kv_append(const gdn_kv_shape* shape, int32_t T, const gdn_bf16* k, int64_t ldk, const gdn_bf16* v, int64_t ldv,
+                  int32_t n_src, const int64_t* slots, const int32_t* rows, uint8_t* k_cache, uint8_t* v_cache,
+                  float* k_scale, float* v_scale, void* stream);
+
+/* Bytes of workspace for gdn_kv_attention (0 on a bad shape).  Depends on Hq,
+ * Hkv and d only. */
+size_t gdn_kv_attention_workspace_bytes(const gdn_kv_shape* shape);
+
+/*
+ * gdn_kv_attention -- attention of a step's query rows over the cache.
+ * For query i of request b (n = start[b+1] - start[b] queries, L = lens[b]
+ * tokens, of which the last n are the queries' own) and head h:
+ *   s_j = scale * (q . k_j),  out = sum_j softmax(s)_j v_j,  lse = log sum_j e^{s_j}
+ * over the tokens j that it sees: j <= L - n + i, or, with tree, j < L - n and
+ * j = L - n + m for the set bits m < 64 of tree[start[b] + i] (bit i among them,
+ * for a node that sees itself).  A query that sees nothing gets out = 0, lse = -inf.
+ *   T      rows of q; rows outside start[0] .. start[B] - 1 are not written.
+ *   q      bf16 [T, Hq, d], ldq elements between rows (a multiple of 8).
+ *   table, start, lens  as gdn_kv_plan leaves them (lens after the step).
+ *   tree   int64 [T], or NULL (causal).
+ *   scale  in (0, 1e6].   k_scale, v_scale positive and finite, 2^-100 .. 2^120
+ *          (a NaN scale makes the rows that see its block NaN, and so does a
+ *          table entry outside the cache).
+ *   out    bf16 [T, Hq, d], rounded once.   lse fp32 [T, Hq], or NULL.
+ *   workspace  device, >= gdn_kv_attention_workspace_bytes(), 256-byte aligned,
+ *          zeroed by the caller before its first use; a call leaves it as the
+ *          next one needs it.  Calls that may overlap need workspaces of their own.
+ *          Its int32 at offset 0 is set non-zero if a bounded device wait
+ *          gave up, and stays so; gdn_kv_attention_status() reads it.
+ * Products are exact in the codes; q and the softmax's weights are held as
+ * two e4m3 numbers each (eight significant bits: bf16's), sums in fp32.  What
+ * lies in the cache past a request's length is never used, whatever its bits.
+ * Results do not depend on timing: the same call gives the same bits.
+ */
+int gdn_kv_attention(const gdn_kv_shape* shape, int32_t T, const gdn_bf16* q, int64_t ldq, const uint8_t* k_cache,
+                     const uint8_t* v_cache, const float* k_scale, const float* v_scale, const int32_t* table,
+                     const int32_t* start, const int32_t* lens, const int64_t* tree, float scale, gdn_bf16* out,
+                     float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* gdn_kv_attention_status -- the status word of the calls that used
+ * `workspace`, read as gdn_prefill_status() reads a prefill's: GDN_OK, or
+ * GDN_ERR_TIMEOUT when a bounded device wait gave up and the results of that call are
+ * not valid (zero the workspace before its next use). */
+int gdn_kv_attention_status(const void* workspace, void* stream, int32_t* status);
+
 #ifdef __cplusplus
 }
 #endif
