@@ -364,18 +364,22 @@ PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
     return fn;
 }
 
-// A cache as rows of d codes, loaded in boxes of 32 rows x 128 bytes with the
+// A cache as rows of d codes, loaded in boxes of `rows` rows x 128 bytes with the
 // 128-byte swizzle (16-byte chunk c of row r lies at c ^ (r & 7)).
-bool encode_cache_map(CUtensorMap* map, const uint8_t* cache, const gdn_kv_shape* s) {
+bool encode_cache_map(CUtensorMap* map, const uint8_t* cache, const gdn_kv_shape* s, int rows) {
     const PFN_cuTensorMapEncodeTiled_v12000 enc = tmap_encoder();
     if (enc == nullptr) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)s->d, (cuuint64_t)s->pages * s->Hkv * s->page};
     const cuuint64_t strides[1] = {(cuuint64_t)s->d};
-    const cuuint32_t box[2] = {128, 32}, unit[2] = {1, 1};
+    const cuuint32_t box[2] = {128, (cuuint32_t)rows}, unit[2] = {1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(cache), dims, strides, box, unit,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+// Which attention kernel: eight rows at a time, or 128.  The first reads a
+// request's cache once for every eight of its rows (queries x heads of a group).
+bool use_tiles(const gdn_kv_shape* s, int T) { return (int64_t)T * (s->Hq / s->Hkv) > (int64_t)8 * s->B; }
 
 }  // namespace
 
@@ -503,7 +507,7 @@ int gdn_kv_append(const gdn_kv_shape* shape, int32_t T, const gdn_bf16* k, int64
 
 size_t gdn_kv_attention_workspace_bytes(const gdn_kv_shape* shape) {
     if (check_kv_shape(shape) != GDN_OK) return 0;
-    return kKvPartialsAt + kv_attn_rows_workspace(shape->d);
+    return kKvPartialsAt + std::max(kv_attn_rows_workspace(shape->d), kv_attn_tiles_workspace(shape->d));
 }
 
 int gdn_kv_attention(const gdn_kv_shape* shape, int32_t T, const gdn_bf16* q, int64_t ldq, const uint8_t* k_cache,
@@ -534,7 +538,9 @@ int gdn_kv_attention(const gdn_kv_shape* shape, int32_t T, const gdn_bf16* q, in
     if (workspace_bytes < need)
         return report_error(GDN_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
     KvAttnParams p{};
-    if (!encode_cache_map(&p.tm_k, k_cache, shape) || !encode_cache_map(&p.tm_v, v_cache, shape))
+    const bool tiles = use_tiles(shape, T);
+    const int box = tiles ? shape->page : 32;
+    if (!encode_cache_map(&p.tm_k, k_cache, shape, box) || !encode_cache_map(&p.tm_v, v_cache, shape, box))
         return report_error(GDN_ERR_CUDA, "the driver refused the cache's tensor maps");
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.q = q;
@@ -560,7 +566,8 @@ int gdn_kv_attention(const gdn_kv_shape* shape, int32_t T, const gdn_bf16* q, in
     p.pages = shape->pages;
     p.log2_page = log2_of(shape->page);
     p.scale_log2 = scale * 1.4426950408889634f;
-    cudaError_t e = launch_kv_attn_rows(p, shape->d, static_cast<cudaStream_t>(stream));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = tiles ? launch_kv_attn_tiles(p, shape->d, st) : launch_kv_attn_rows(p, shape->d, st);
     return e == cudaSuccess ? GDN_OK : cuda_error(e, "cache attention launch");
 }
 

@@ -64,7 +64,7 @@ struct KvAppendParams {
 };
 
 struct KvAttnParams {
-    CUtensorMap tm_k, tm_v;     // the caches as [pages * Hkv * P, d] bytes, 128-byte wide boxes
+    CUtensorMap tm_k, tm_v;     // the caches as [pages * Hkv * P, d] bytes, in boxes of 128 bytes x 32 rows, or x a page
     const uint16_t* q;          // bf16 rows [T, Hq, d], row stride ldq
     const float* k_scale;       // [pages, Hkv]
     const float* v_scale;
@@ -92,6 +92,9 @@ cudaError_t launch_kv_plan(const KvPlanParams& p, cudaStream_t s);
 // One to eight query rows of a key/value head at a time (mma.sync).
 cudaError_t launch_kv_attn_rows(KvAttnParams& p, int d, cudaStream_t s);
 size_t kv_attn_rows_workspace(int d);
+// 128 query rows at a time (tcgen05).
+cudaError_t launch_kv_attn_tiles(KvAttnParams& p, int d, cudaStream_t s);
+size_t kv_attn_tiles_workspace(int d);
 
 #ifdef __CUDACC__
 // 2^e for e in the normal range.

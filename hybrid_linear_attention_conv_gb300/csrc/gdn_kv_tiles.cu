@@ -1,0 +1,644 @@
+// gdn_kv_tiles.cu -- attention over the paged 8-bit cache for many query rows:
+// 128 rows (queries x heads of one key/value head) against 128 tokens at a
+// time on the tcgen05 tensor cores.  The mathematics is gdn_kv_rows.cu's: with
+// a_j, b_j the scales of token j's blocks,
+//   t_j = scale log2(e) a_j (q . c_j) + log2 b_j,   o = sum 2^(t_j - m) w_j / sum 2^(t_j - m) / b_j.
+//
+// Both products take the cache's codes as they are (kind::f8f6f4): q and the
+// weights are split into two e4m3 numbers, hi + lo, and every contraction runs
+// over both, twice the products at twice bf16's rate, with half its bytes
+// of operands and no conversion of a tile.
+//
+// Roles of the CTA's fourteen warps: one loads tiles (TMA) and their scales;
+// one thread issues the MMAs; eight are the softmax, in two halves of 64
+// columns, so that a tile's weights are ready within the time its neighbours'
+// MMAs take; four split the next item's q while the last tiles run.
+// Tensor memory: two tiles of logits (2 x 128 columns), over which their
+// weights are written as the second product's A operand, and the output
+// (d columns).  Per tile j the tensor pipe runs S(j + 1), then O += P(j) V(j).
+//
+// The reference m of a row is raised, and the output rescaled in tensor
+// memory, only when a tile's maximum exceeds it by more than 2^3.8: weights
+// are held times 2^5, so they stay below e4m3's 448, and the smallest step of
+// lo is 2^-14 of a weight of 1.
+//
+// The list of all (request, row tile, head, token tile) is cut evenly over
+// the CTAs, one to an SM, causal tiles that nobody sees left out; an item that
+// spans several CTAs is joined by the last of them to finish, in CTA order.
+#include <algorithm>
+#include <mutex>
+
+#include "gdn_kv.cuh"
+#include "gdn_kv_tc.cuh"
+#include "gdn_tc.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kSoftWarps = 8, kQWarps = 4;
+constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kQWarp0 = kSoftWarps + 2;
+constexpr int kThreads = (kSoftWarps + 2 + kQWarps) * 32;
+constexpr int kM = 128;                 // rows of an item
+constexpr int kN = 128;                 // tokens of a tile
+constexpr float kPExp = 5.0f;           // weights are held times 2^5
+constexpr float kGrow = 3.8f;           // 2^(5 + 3.8) = 446
+constexpr int kScaleRing = 8;
+constexpr int kMinTiles = 2;            // tiles a CTA takes at least
+constexpr uint64_t kDrainNs = 200000000ull;
+
+template <int D>
+struct TilesSmem {
+    static constexpr int kSlot = kN * D;                      // a tile's keys or values
+    static constexpr int kSlots = D == 256 ? 4 : 8;
+    alignas(1024) uint8_t q[2][kM * D];                       // hi, lo
+    alignas(1024) uint8_t ring[kSlots][kSlot];
+    float4 scales[kScaleRing][2];                             // {key scale, log2 value scale} of 4 x 32 tokens
+    float rf[kM];
+    float red[2][2][kM];
+    alignas(8) uint64_t full[kSlots], empty[kSlots], s_full[2], p_ready[2], scales_full[kScaleRing];
+    uint64_t q_full, q_empty, o_done, o_free, drained;
+    long long scan[kThreads / 32];
+    int qbase[kThreads];
+    int at_b, at_t, at_h, at_j;
+    unsigned last;
+    uint32_t tmem;
+    int dead;
+};
+
+struct Request {
+    int n, L, row0, tiles;  // queries, tokens, first row of q, row tiles
+};
+
+__device__ __forceinline__ Request request(const KvAttnParams& p, int b) {
+    Request r;
+    r.row0 = p.start[b];
+    r.n = max(0, min(p.start[b + 1], p.T) - r.row0);
+    if (r.row0 < 0) r.n = 0;
+    r.L = max(0, min(p.lens[b], p.width << p.log2_page));
+    r.tiles = (r.n * p.G + kM - 1) / kM;
+    return r;
+}
+
+// Token tiles that some row of row tile t sees (at least one).
+__device__ __forceinline__ int token_tiles(const KvAttnParams& p, const Request& r, int t) {
+    const int last = min(r.n - 1, (t * kM + kM - 1) / p.G);
+    const int seen = p.tree != nullptr ? r.L : min(r.L, r.L - r.n + last + 1);
+    return max(1, (seen + kN - 1) / kN);
+}
+
+// One stretch of an item's token tiles, and the walk over a CTA's stretches.
+struct Walk {
+    int b, t, h, j0, j1, kt;
+    long long x, x1;
+    Request r;
+    __device__ __forceinline__ bool settle(const KvAttnParams& p) {  // false: the CTA's part is done
+        if (x >= x1) return false;
+        r = request(p, b);
+        while (t >= r.tiles) {
+            t = 0;
+            ++b;
+            r = request(p, b);
+        }
+        kt = token_tiles(p, r, t);
+        j1 = (int)min((long long)kt, j0 + (x1 - x));
+        return true;
+    }
+    __device__ __forceinline__ void advance(const KvAttnParams& p) {
+        x += j1 - j0;
+        j0 = 0;
+        if (j1 == kt && ++h == p.Hkv) {
+            h = 0;
+            ++t;
+        }
+    }
+};
+
+__device__ __forceinline__ float factor(float m, float top) { return m == top ? 1.0f : ex2(m - top); }
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __grid_constant__ KvAttnParams p) {
+    using Smem = TilesSmem<D>;
+    constexpr int kSlot = Smem::kSlot, kSlots = Smem::kSlots, kHalves = D / 128;
+    constexpr uint32_t kHalfBytes = kN * 128;
+    constexpr int kPart = kM * D + 2 * kM;
+    extern __shared__ uint8_t smem_raw[];
+    Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    // ---- this CTA's part of the list
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int rb0 = min(tid * per, p.B), rb1 = min(rb0 + per, p.B);
+    auto scan = [&](long long v, long long& total) {  // exclusive prefix over the CTA's threads
+        long long u = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long w = __shfl_up_sync(~0u, u, o);
+            if (lane >= o) u += w;
+        }
+        if (lane == 31) sm.scan[warp] = u;
+        __syncthreads();
+        total = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) u += sm.scan[w];
+            total += sm.scan[w];
+        }
+        __syncthreads();
+        return u - v;
+    };
+    long long mine = 0, total = 0;
+    for (int b = rb0; b < rb1; ++b) mine += request(p, b).tiles;
+    sm.qbase[tid] = (int)scan(mine, total);
+    __syncthreads();
+    const int nq = (int)total, perq = (nq + kThreads - 1) / kThreads;
+    const int q0 = min(tid * perq, nq), q1 = min(q0 + perq, nq);
+    int b0 = 0, t0 = 0;  // the first of this thread's row tiles
+    mine = 0;
+    if (q0 < q1) {
+        int lo = 0, hi = kThreads;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (sm.qbase[mid] <= q0) lo = mid;
+            else hi = mid;
+        }
+        b0 = lo * per;
+        t0 = q0 - sm.qbase[lo];
+        Request r = request(p, b0);
+        for (; t0 >= r.tiles; r = request(p, ++b0)) t0 -= r.tiles;
+        int b = b0, t = t0;
+        for (int q = q0; q < q1; ++q, ++t) {
+            while (t >= r.tiles) {
+                t = 0;
+                r = request(p, ++b);
+            }
+            mine += token_tiles(p, r, t);
+        }
+    }
+    const long long before = scan(mine, total) * p.Hkv;
+    total *= p.Hkv;
+    const long long W = max((total + gridDim.x - 1) / gridDim.x, (long long)kMinTiles);
+    const long long x0 = blockIdx.x * W, x1 = min(x0 + W, total);
+    if (x0 >= x1) return;  // uniform; nothing is in flight
+    if (before <= x0 && x0 < before + mine * p.Hkv) {
+        long long rest = x0 - before;
+        int b = b0, t = t0;
+        Request r = request(p, b);
+        for (;; ++t) {
+            while (t >= r.tiles) {
+                t = 0;
+                r = request(p, ++b);
+            }
+            const int kt = token_tiles(p, r, t);
+            if (rest < (long long)kt * p.Hkv) {
+                sm.at_b = b;
+                sm.at_t = t;
+                sm.at_h = (int)(rest / kt);
+                sm.at_j = (int)(rest % kt);
+                break;
+            }
+            rest -= (long long)kt * p.Hkv;
+        }
+    }
+
+    // ---- barriers and tensor memory
+    const uint32_t full = tc::smem_u32(sm.full), empty = tc::smem_u32(sm.empty), s_full = tc::smem_u32(sm.s_full),
+                   p_ready = tc::smem_u32(sm.p_ready), scales_full = tc::smem_u32(sm.scales_full),
+                   q_full = tc::smem_u32(&sm.q_full), q_empty = tc::smem_u32(&sm.q_empty),
+                   o_done = tc::smem_u32(&sm.o_done), o_free = tc::smem_u32(&sm.o_free),
+                   drained = tc::smem_u32(&sm.drained);
+    if (tid == 0) {
+        sm.dead = 0;
+        for (int i = 0; i < kSlots; ++i) {
+            tc::mbar_init(full + 8 * i, 1);
+            tc::mbar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(s_full + 8 * i, 1);
+            tc::mbar_init(p_ready + 8 * i, kSoftWarps);
+        }
+        for (int i = 0; i < kScaleRing; ++i) tc::mbar_init(scales_full + 8 * i, 1);
+        tc::mbar_init(q_full, kQWarps);
+        tc::mbar_init(q_empty, 1 + kSoftWarps);
+        tc::mbar_init(o_done, 1);
+        tc::mbar_init(o_free, kSoftWarps);
+        tc::mbar_init(drained, 1);
+    }
+    if (warp == kMmaWarp) tc::tmem_alloc(tc::smem_u32(&sm.tmem), 512);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = sm.tmem, tO = tmem + 256;  // logits and weights in columns 0 .. 255
+    volatile int* dead = &sm.dead;
+
+    // A bounded wait.  The first that gives up ends all waiting (and all
+    // copies and MMAs) of the CTA: the roles run through, the status word tells.
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (*dead) return;
+        if (!tc::mbar_wait(bar, parity & 1, p.wait_ns)) {
+            *dead = 1;
+            atomicOr(p.status, 2);
+        }
+    };
+
+    Walk w;
+    w.b = sm.at_b;
+    w.t = sm.at_t;
+    w.h = sm.at_h;
+    w.j0 = sm.at_j;
+    w.x = x0;
+    w.x1 = x1;
+
+    if (warp == kLoadWarp) {
+        // ------------------------------------------------------------ tiles
+        const int page_rows = min(1 << p.log2_page, kN), boxes = kN / page_rows;
+        int u = 0, g = 0;  // ring units (keys, values), tiles
+        for (; w.settle(p); w.advance(p)) {
+            // eight tiles' places and scales at a time: lane = 4 tile + 32-token stretch
+            int y = 0, y_next = 0;
+            float ks = 0.0f, lv = 0.0f, ks_next = 0.0f, lv_next = 0.0f;
+            auto lookup = [&](int j) {
+                const int pos = (j + (lane >> 2)) * kN + (lane & 3) * 32, idx = pos >> p.log2_page;
+                const int page = pos < w.r.L && idx < p.width ? p.table[(int64_t)w.b * p.width + idx] : -1;
+                const bool good = page >= 0 && page < p.pages;
+                y_next = cache_row(page, p.pages, p.Hkv, w.h, p.log2_page, pos);
+                ks_next = good ? p.k_scale[(int64_t)page * p.Hkv + w.h] : __int_as_float(0x7fffffff);
+                lv_next = good ? log2f(p.v_scale[(int64_t)page * p.Hkv + w.h]) : __int_as_float(0x7fffffff);
+            };
+            lookup(w.j0);
+            for (int j = w.j0; j < w.j1; ++j, ++g) {
+                const int k = (j - w.j0) & 7;
+                if (k == 0) {
+                    y = y_next;
+                    ks = ks_next;
+                    lv = lv_next;
+                    lookup(j + 8);
+                }
+                float* sc = reinterpret_cast<float*>(sm.scales[g % kScaleRing]);
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv, ++u) {
+                    const int slot = u % kSlots;
+                    if (u >= kSlots) wait(empty + 8 * slot, u / kSlots - 1);
+                    if (kv == 0) {
+                        // the place in the ring is free: its last readers were done before the
+                        // weights of the tile whose keys lay in this slot were
+                        if ((lane >> 2) == k) {
+                            sc[2 * (lane & 3)] = ks;
+                            sc[2 * (lane & 3) + 1] = lv;
+                        }
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(scales_full + 8 * (g % kScaleRing));
+                    }
+                    if (*dead) continue;
+                    const uint32_t dst = tc::smem_u32(sm.ring[slot]);
+                    if (lane == 0) tc::mbar_arrive_expect_tx(full + 8 * slot, kSlot);
+                    for (int i = 0; i < boxes; ++i) {
+                        const int row = __shfl_sync(~0u, y, 4 * k + i * (4 / boxes));
+                        if (lane == 0)
+#pragma unroll
+                            for (int hf = 0; hf < kHalves; ++hf)
+                                tc::tma_load_2d(dst + hf * kHalfBytes + i * page_rows * 128, kv ? &p.tm_v : &p.tm_k, hf * 128, row,
+                                                full + 8 * slot);
+                    }
+                }
+            }
+        }
+        // Copies that nobody waited for (after a wait that gave up) land before the CTA ends.
+        if (*dead && lane == 0)
+            for (int i = 0; i < kSlots; ++i)
+                for (uint32_t par = 0; par < 2; ++par) tc::mbar_wait(full + 8 * i, par, kDrainNs / 20);
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------- MMAs
+        if (lane == 0) {
+            constexpr uint32_t id_s = tc::idesc_e4m3(kM, kN, false), id_o = tc::idesc_e4m3(kM, D, true);
+            const uint32_t q_hi = tc::smem_u32(sm.q[0]), q_lo = tc::smem_u32(sm.q[1]);
+            int g = 0, item = 0;
+            bool pending = false, pend_first = false;  // the weights' product of tile g - 1
+            int pend_item = 0;
+            auto product = [&]() {
+                if (!pending) return;
+                pending = false;
+                const int gp = g - 1, u = 2 * gp + 1, slot = u % kSlots, buf = gp & 1;
+                if (pend_first && pend_item > 0) wait(o_free, pend_item - 1);
+                wait(full + 8 * slot, u / kSlots);
+                wait(p_ready + 8 * buf, gp >> 1);
+                if (*dead) return;
+                tc::fence_after_sync();
+                const uint32_t v = tc::smem_u32(sm.ring[slot]), a = tmem + buf * 128;
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int ks = 0; ks < kN / 32; ++ks)
+                        tc::mma_e4m3_ts(tO, a + part * 32 + ks * 8, tc::smem_desc_mn_sw128(v + ks * 32 * 128, kHalfBytes), id_o,
+                                        !(pend_first && part == 0 && ks == 0));
+                tc::mma_commit(empty + 8 * slot);
+                tc::mma_commit(o_done);
+            };
+            for (; w.settle(p); w.advance(p), ++item) {
+                // the last item's product first, unless this item's q is there already
+                if (!tc::mbar_test(q_full, item & 1)) product();
+                wait(q_full, item);
+                for (int j = w.j0; j < w.j1; ++j) {
+                    const int u = 2 * g, slot = u % kSlots, buf = g & 1;
+                    wait(full + 8 * slot, u / kSlots);
+                    if (!*dead) {
+                        tc::fence_after_sync();
+                        const uint32_t k = tc::smem_u32(sm.ring[slot]);
+#pragma unroll
+                        for (int part = 0; part < 2; ++part)
+#pragma unroll
+                            for (int ks = 0; ks < D / 32; ++ks) {
+                                const uint32_t at = (ks >> 2) * kHalfBytes + (ks & 3) * 32;
+                                tc::mma_e4m3(tmem + buf * 128, tc::smem_desc_sw128((part ? q_lo : q_hi) + at), tc::smem_desc_sw128(k + at),
+                                             id_s, part + ks > 0);
+                            }
+                        tc::mma_commit(empty + 8 * slot);
+                        tc::mma_commit(s_full + 8 * buf);
+                        if (j == w.j1 - 1) tc::mma_commit(q_empty);
+                    }
+                    product();
+                    ++g;
+                    pending = true;
+                    pend_first = j == w.j0;
+                    pend_item = item;
+                }
+            }
+            product();
+            // every MMA has ended before tensor memory is given back
+            tc::mma_commit(drained);
+            tc::mbar_wait(drained, 0, kDrainNs);
+        }
+        __syncwarp();
+    } else if (warp >= kQWarp0) {
+        // ----------------------------------------------------------- queries
+        constexpr int kLanes = D / 16;              // of a row, 16 values each
+        constexpr int kAtOnce = 32 / kLanes;        // rows of a warp's step
+        const int sub = lane / kLanes, c = lane % kLanes;
+        int item = 0;
+        for (; w.settle(p); w.advance(p), ++item) {
+            if (item > 0) wait(q_empty, item - 1);
+            const int rows = w.r.n * p.G;
+#pragma unroll 4
+            for (int i = 0; i < 32 / kAtOnce; ++i) {
+                const int local = (warp - kQWarp0) * 32 + i * kAtOnce + sub, row = w.t * kM + local;
+                uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                if (row < rows) {
+                    const int qi = row / p.G, head = w.h * p.G + row - qi * p.G;
+                    const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(w.r.row0 + qi) * p.ldq + (int64_t)head * D) + 2 * c;
+                    x[0] = src[0];
+                    x[1] = src[1];
+                }
+                const uint32_t word[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+                uint32_t m2 = 0;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) m2 = __vmaxu2(m2, word[k] & 0x7fff7fffu);
+                uint32_t top = max(m2 & 0xffffu, m2 >> 16);
+#pragma unroll
+                for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+                const bool finite = top < 0x7f80u;
+                const int e = finite ? scale_exp_of_bf16(top) : 0;
+                const float inv = exp2_int(-e);
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t a = finite ? word[2 * k] : 0u, b = finite ? word[2 * k + 1] : 0u;
+                    const float f[4] = {__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xffff0000u) * inv,
+                                        __uint_as_float(b << 16) * inv, __uint_as_float(b & 0xffff0000u) * inv};
+                    split4_e4m3(f, hi[k], lo[k]);
+                }
+                const uint32_t at = (c >> 3) * (kM * 128) + local * 128 + (((c & 7) ^ (local & 7)) << 4);
+                *reinterpret_cast<uint4*>(sm.q[0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(sm.q[1] + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                // a query that is not finite makes its row NaN, through the row's factor
+                if (c == 0) sm.rf[local] = finite ? exp2_int(e) * p.scale_log2 : __int_as_float(0x7fffffff);
+            }
+            tc::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(q_full);
+        }
+    } else {
+        // ----------------------------------------------------------- softmax
+        const int quad = warp & 3, half = warp >> 2, local = quad * 32 + lane;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        int g = 0, item = 0;
+        for (; w.settle(p); w.advance(p), ++item) {
+            const int row = w.t * kM + local;
+            const bool have = row < w.r.n * p.G;
+            const int qi = have ? row / p.G : 0, head = w.h * p.G + (have ? row - qi * p.G : 0);
+            const int base = w.r.L - w.r.n;
+            const int seen = have ? base + qi + 1 : 0;
+            const unsigned long long tree = p.tree != nullptr && have ? (unsigned long long)p.tree[w.r.row0 + qi] : 0ull;
+            const int all_see = max(0, min(w.r.L, p.tree != nullptr ? base : base + (w.t * kM) / p.G + 1));
+            wait(q_full, item);
+            const float rf = sm.rf[local];
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(q_empty);
+            float m = -INFINITY, l = 0.0f;
+            for (int j = w.j0; j < w.j1; ++j, ++g) {
+                const int buf = g & 1, pos0 = j * kN + half * 64;
+                wait(scales_full + 8 * (g % kScaleRing), g / kScaleRing);
+                const float4 sc = sm.scales[g % kScaleRing][half];  // two stretches of 32 tokens
+                wait(s_full + 8 * buf, g >> 1);
+                tc::fence_after_sync();
+                float s[64];
+                tc::tmem_ld64(tmem + lanes + buf * 128 + half * 64, s);
+                float f0 = rf * sc.x, v0 = sc.y, f1 = rf * sc.z, v1 = sc.w;
+                if (j * kN + kN > all_see) {  // some row does not see some token: the logits themselves
+#pragma unroll
+                    for (int k = 0; k < 64; ++k) {
+                        const int pos = pos0 + k, node = pos - base;
+                        const bool vis = p.tree != nullptr ? have && pos < w.r.L && (node < 0 || (node < 64 && ((tree >> (node & 63)) & 1)))
+                                                           : pos < seen;
+                        s[k] = vis ? fmaf(s[k], k < 32 ? f0 : f1, k < 32 ? v0 : v1) : -INFINITY;
+                    }
+                    f0 = f1 = 1.0f;
+                    v0 = v1 = 0.0f;
+                }
+                float top0 = s[0], top1 = s[32];
+#pragma unroll
+                for (int k = 1; k < 32; ++k) {
+                    top0 = fmaxf(top0, s[k]);
+                    top1 = fmaxf(top1, s[k + 32]);
+                }
+                float top = fmaxf(fmaf(top0, f0, v0), fmaf(top1, f1, v1));
+                sm.red[buf][half][local] = top;
+                tc::named_sync(1 + quad, 64);  // both halves have read their logits, too
+                top = fmaxf(top, sm.red[buf][half ^ 1][local]);
+                const bool grows = m > -INFINITY && top > m + kGrow;
+                if (m == -INFINITY) m = fmaxf(m, top);
+                if (__any_sync(~0u, grows)) {
+                    const float c = grows ? ex2(m - top) : 1.0f;
+                    if (grows) m = top;
+                    l *= c;
+                    if (j > w.j0) {
+                        wait(o_done, g - 1);
+                        tc::fence_after_sync();
+#pragma unroll 1
+                        for (int k = 0; k < D / 64; ++k) {
+                            float o[32];
+                            tc::tmem_ld32(tO + lanes + half * (D / 2) + 32 * k, o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] *= c;
+                            tc::tmem_st32(tO + lanes + half * (D / 2) + 32 * k, o);
+                        }
+                    }
+                }
+                const float shift = kPExp - (m == -INFINITY ? 0.0f : m);
+                const float a0 = v0 + shift, a1 = v1 + shift;
+                float sum0 = 0.0f, sum1 = 0.0f;
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const float f = k < 8 ? f0 : f1, a = k < 8 ? a0 : a1;
+                    const float e[4] = {ex2(fmaf(s[4 * k], f, a)), ex2(fmaf(s[4 * k + 1], f, a)), ex2(fmaf(s[4 * k + 2], f, a)),
+                                        ex2(fmaf(s[4 * k + 3], f, a))};
+                    if (k < 8) sum0 += (e[0] + e[1]) + (e[2] + e[3]);
+                    else sum1 += (e[0] + e[1]) + (e[2] + e[3]);
+                    split4_e4m3(e, hi[k], lo[k]);
+                }
+                tc::tmem_st16(tmem + lanes + buf * 128 + half * 16, hi);
+                tc::tmem_st16(tmem + lanes + buf * 128 + 32 + half * 16, lo);
+                if (sum0 != 0.0f) l = fmaf(sum0, ex2(-sc.y), l);  // a row that sees nothing here takes nothing from the block's scale
+                if (sum1 != 0.0f) l = fmaf(sum1, ex2(-sc.w), l);
+                if (j * kN + kN > w.r.L) {  // whatever lies past the end: zeros for the product
+                    const int u = 2 * g + 1, slot = u % kSlots;
+                    wait(full + 8 * slot, u / kSlots);
+                    const int first = max(0, w.r.L - j * kN);
+                    for (int i = tid; i < (kN - first) * (D / 16); i += kSoftWarps * 32) {
+                        const int tok = first + i / (D / 16), c = i % (D / 16);
+                        *reinterpret_cast<uint4*>(sm.ring[slot] + (c >> 3) * kHalfBytes + tok * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    tc::fence_async_smem();
+                }
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(p_ready + 8 * buf);
+            }
+
+            // ---- the item's output: whole, or this CTA's part of it
+            sm.red[g & 1][half][local] = l;
+            tc::named_sync(1 + quad, 64);
+            l += sm.red[g & 1][half ^ 1][local];
+            tc::named_sync(1 + quad, 64);  // read before the next item writes there
+            const long long item0 = w.x - w.j0;
+            const int c0 = (int)(item0 / W), c1 = (int)((item0 + w.kt - 1) / W);
+            const int64_t at = (int64_t)(w.r.row0 + qi) * p.Hq + head;
+            auto put = [&](int k, const float (&o)[32], float inv) {  // columns half * D / 2 + 32 k ..
+                if (!have) return;
+                uint16_t* dst = p.out + at * D + half * (D / 2) + 32 * k;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t u[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        u[e] = tc::pack_bf16(__float2bfloat16_rn(o[8 * i + 2 * e] * inv), __float2bfloat16_rn(o[8 * i + 2 * e + 1] * inv));
+                    reinterpret_cast<uint4*>(dst)[i] = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+            };
+            auto put_lse = [&]() {
+                if (p.lse != nullptr && have && half == 0)
+                    p.lse[at] = l == 0.0f ? -INFINITY : ((m == -INFINITY ? 0.0f : m) - kPExp + log2f(l)) * 0.69314718055994531f;
+            };
+            wait(o_done, g - 1);
+            tc::fence_after_sync();
+            if (c0 == c1) {
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no token seen: zeros
+#pragma unroll 1
+                for (int k = 0; k < D / 64; ++k) {
+                    float o[32];
+                    tc::tmem_ld32(tO + lanes + half * (D / 2) + 32 * k, o);
+                    put(k, o, inv);
+                }
+                put_lse();
+            } else {
+                float* part = p.partials + ((size_t)blockIdx.x * 2 + (w.j0 == 0 ? 1 : 0)) * kPart;
+#pragma unroll 1
+                for (int k = 0; k < D / 64; ++k) {
+                    float o[32];
+                    tc::tmem_ld32(tO + lanes + half * (D / 2) + 32 * k, o);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        reinterpret_cast<float4*>(part)[(half * (D / 8) + 8 * k + i) * kM + local] =
+                            make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                }
+                if (half == 0) {
+                    part[kM * D + local] = m;
+                    part[kM * D + kM + local] = l;
+                }
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(o_free);
+            if (c0 != c1) {
+                __threadfence();
+                tc::named_sync(5, kSoftWarps * 32);
+                if (tid == 0) {
+                    const unsigned n = atomicAdd(p.counters + c0, 1u);
+                    sm.last = n == (unsigned)(c1 - c0);
+                    if (sm.last) p.counters[c0] = 0;  // as the next call finds it
+                    __threadfence();
+                }
+                tc::named_sync(5, kSoftWarps * 32);
+                const bool join = sm.last != 0;
+                tc::named_sync(5, kSoftWarps * 32);
+                if (join) {
+                    auto part_of = [&](int c) { return p.partials + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * kPart; };
+                    m = -INFINITY;
+                    for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(part_of(c) + kM * D + local));
+                    l = 0.0f;
+                    for (int c = c0; c <= c1; ++c)
+                        l = fmaf(__ldcg(part_of(c) + kM * D + kM + local), factor(__ldcg(part_of(c) + kM * D + local), m), l);
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+                    for (int k = 0; k < D / 64; ++k) {
+                        float o[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+                        for (int c = c0; c <= c1; ++c) {
+                            const float f = factor(__ldcg(part_of(c) + kM * D + local), m);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 v = __ldcg(reinterpret_cast<const float4*>(part_of(c)) + (half * (D / 8) + 8 * k + i) * kM + local);
+                                o[4 * i] = fmaf(v.x, f, o[4 * i]);
+                                o[4 * i + 1] = fmaf(v.y, f, o[4 * i + 1]);
+                                o[4 * i + 2] = fmaf(v.z, f, o[4 * i + 2]);
+                                o[4 * i + 3] = fmaf(v.w, f, o[4 * i + 3]);
+                            }
+                        }
+                        put(k, o, inv);
+                    }
+                    put_lse();
+                }
+            }
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch(KvAttnParams& p, cudaStream_t s) {
+    constexpr int smem = (int)sizeof(TilesSmem<D>) + 1024;
+    static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+    static std::once_flag once[64];
+    static cudaError_t err[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= 64) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+    std::call_once(once[dev], [dev] {
+        err[dev] = cudaFuncSetAttribute(gdn_kv_attn_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    });
+    if (err[dev] != cudaSuccess) return err[dev];
+    const int grid = std::min(device_sm_count(), kKvMaxCtas);
+    gdn_kv_attn_tiles_kernel<D><<<grid, kThreads, smem, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t kv_attn_tiles_workspace(int d) { return (size_t)2 * std::min(device_sm_count(), kKvMaxCtas) * (kM * d + 2 * kM) * 4; }
+
+cudaError_t launch_kv_attn_tiles(KvAttnParams& p, int d, cudaStream_t s) { return d == 256 ? launch<256>(p, s) : launch<128>(p, s); }
+
+}  // namespace gdn

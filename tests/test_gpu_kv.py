@@ -324,18 +324,21 @@ class Step:
         self.tree = torch.tensor([w - (1 << 64) if w >> 63 else w for w in words], dtype=torch.int64, device=DEV)
         return self
 
-    def run(self, scale=None, workspace=None):
-        out = torch.full((self.T + 2, self.Hq, self.d), 7.0, dtype=torch.bfloat16, device=DEV)  # rows that no request has stay
-        lse = torch.full((self.T + 2, self.Hq), 7.0, device=DEV)
-        q = torch.cat([self.q, self.q.new_zeros((2, self.Hq, self.d))]) if self.T else self.q.new_zeros((2, self.Hq, self.d))
-        tree = None if self.tree is None else torch.cat([self.tree, self.tree.new_zeros(2)])
+    def run(self, scale=None, workspace=None, pad=2):
+        """pad: rows of q past the requests' own.  The number of rows picks the kernel (eight rows
+        at a time up to eight a request and key/value head, 128 above), so pad=0 and pad=2 of a few
+        single tokens run both."""
+        out = torch.full((self.T + pad, self.Hq, self.d), 7.0, dtype=torch.bfloat16, device=DEV)  # rows that no request has stay
+        lse = torch.full((self.T + pad, self.Hq), 7.0, device=DEV)
+        q = torch.cat([self.q, self.q.new_zeros((pad, self.Hq, self.d))])
+        tree = None if self.tree is None else torch.cat([self.tree, self.tree.new_zeros(pad)])
         gdn.kv_attention(q, *self.cache, self.table, self.start, self.lens, scale=scale, tree=tree, out=out, lse=lse, workspace=workspace)
         torch.cuda.synchronize()
         assert (out[self.T:] == 7.0).all() and (lse[self.T:] == 7.0).all()
         return out[:self.T], lse[:self.T]
 
-    def check(self, scale=None, got=None):
-        out, lse = got or self.run(scale)
+    def check(self, scale=None, got=None, pad=2):
+        out, lse = got or self.run(scale, pad=pad)
         scale = self.d ** -0.5 if scale is None else scale
         G = self.Hq // self.Hkv
         kc, vc = (c.view(torch.uint8) for c in self.cache[:2])
@@ -391,9 +394,10 @@ SHAPES = [(24, 4, 256), (8, 8, 128), (16, 2, 128), (3, 1, 256), (32, 8, 128), (1
 
 @pytest.mark.parametrize("Hq,Hkv,d", SHAPES)
 @pytest.mark.parametrize("page", [32, 64, 128])
-def test_attention_one_token(Hq, Hkv, d, page):
+@pytest.mark.parametrize("pad", [0, 200])
+def test_attention_one_token(Hq, Hkv, d, page, pad):
     lens = [1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 500, 1025]
-    Step(lens, [1] * len(lens), Hq, Hkv, d, page, seed=page + d).check()
+    Step(lens, [1] * len(lens), Hq, Hkv, d, page, seed=page + d).check(pad=pad)
 
 
 @pytest.mark.parametrize("Hq,Hkv,d", SHAPES)
@@ -425,13 +429,14 @@ def test_attention_rows_that_see_nothing():
 @pytest.mark.parametrize("sharp,v_exp", [(8.0, (-9, -5)), (0.01, (-9, -5)), (1.0, (-60, 40)), (30.0, (-20, 20))])
 @pytest.mark.parametrize("new", [1, 150])
 def test_attention_peaked_flat_and_mixed_scales(sharp, v_exp, new):
-    Step([2000, 555], [new, min(new, 20)], 12, 2, 128, 64, seed=8, sharp=sharp, v_exp=v_exp).check()
-    Step([700], [new], 6, 1, 256, 128, seed=9, sharp=sharp, v_exp=v_exp).check()
+    for pad in (0, 2):
+        Step([2000, 555], [new, min(new, 20)], 12, 2, 128, 64, seed=8, sharp=sharp, v_exp=v_exp).check(pad=pad)
+        Step([700], [new], 6, 1, 256, 128, seed=9, sharp=sharp, v_exp=v_exp).check(pad=pad)
 
 
 def test_attention_growing_maximum():
     """Logits that rise along the context: every tile brings a new maximum."""
-    for new in (1, 140):
+    for new, pad in ((1, 0), (1, 2), (140, 2)):
         s = Step([3000], [new], 8, 1, 128, 64, seed=10)
         ramp = torch.linspace(0, 400, 64 * 48, device=DEV)[:s.page * s.table.shape[1]]
         s.q = torch.zeros_like(s.q)
@@ -441,33 +446,35 @@ def test_attention_growing_maximum():
             s.cache[0][pg, 0, :, 0] = ramp[j * 64:(j + 1) * 64].to(torch.float8_e4m3fn)
         s.cache[0].view(torch.uint8).masked_fill_(~s.owned[:, None, :, None], NAN_CODE)
         s.cache[2].fill_(1.0)
-        s.check(scale=0.5)
+        s.check(scale=0.5, pad=pad)
 
 
 @pytest.mark.parametrize("Hq,Hkv,d,new", [(24, 4, 256, 1), (24, 4, 256, 32), (8, 2, 128, 1), (32, 8, 128, 700)])
-def test_attention_long_context_and_same_bits(Hq, Hkv, d, new):
+@pytest.mark.parametrize("pad", [0, 2])
+def test_attention_long_context_and_same_bits(Hq, Hkv, d, new, pad):
     s = Step([20011], [new], Hq, Hkv, d, 64, seed=12)
     ws = torch.zeros(gdn.kv_attention_workspace_bytes(Hq, Hkv, d), dtype=torch.uint8, device=DEV)
-    first = s.check(got=s.run(workspace=ws))
+    first = s.check(got=s.run(workspace=ws, pad=pad))
     for _ in range(3):
-        again = s.run(workspace=ws)
+        again = s.run(workspace=ws, pad=pad)
         assert torch.equal(first[0].view(torch.int16), again[0].view(torch.int16)) and torch.equal(first[1], again[1])
     assert gdn.kv_attention_status(ws) == 0
 
 
 def test_attention_many_requests():
     lens = [(37 * i) % 700 for i in range(300)]
-    Step(lens, [1 if x else 0 for x in lens], 8, 2, 128, 32, seed=13).check()
+    for pad in (0, 2000):
+        Step(lens, [1 if x else 0 for x in lens], 8, 2, 128, 32, seed=13).check(pad=pad)
 
 
-@pytest.mark.parametrize("new", [1, 40])
-def test_attention_not_a_number_stays_in_its_rows(new):
+@pytest.mark.parametrize("new,pad", [(1, 0), (1, 2), (40, 2)])
+def test_attention_not_a_number_stays_in_its_rows(new, pad):
     s = Step([200, 90], [new, 1], 16, 2, 128, 64, seed=14)
-    clean = s.run()
+    clean = s.run(pad=pad)
     # a query
     q = s.q.clone()
     s.q[new // 2, 3, 5] = math.inf
-    out, lse = s.run()
+    out, lse = s.run(pad=pad)
     rows = torch.zeros(out.shape[:2], dtype=torch.bool, device=DEV)
     rows[new // 2, 3] = True
     assert torch.isnan(out[rows]).all() and torch.isnan(lse[rows]).all()
@@ -477,7 +484,7 @@ def test_attention_not_a_number_stays_in_its_rows(new):
     for which in (2, 3):
         keep = s.cache[which].clone()
         s.cache[which][int(s.table[0, 3]), 1] = math.nan
-        out, lse = s.run()
+        out, lse = s.run(pad=pad)
         rows[:] = False
         for i in range(new):
             if 200 - new + i >= 192:
@@ -489,7 +496,7 @@ def test_attention_not_a_number_stays_in_its_rows(new):
     for entry in (-1, s.pages, 2 ** 31 - 1, -2 ** 31):
         keep = s.table.clone()
         s.table[0, 3] = entry
-        out, lse = s.run()
+        out, lse = s.run(pad=pad)
         rows[:] = False
         for i in range(new):
             if 200 - new + i >= 192:
@@ -501,15 +508,17 @@ def test_attention_not_a_number_stays_in_its_rows(new):
 def test_attention_length_past_the_table_is_cut():
     """lens beyond the table's width: what the table has counts, and nothing else is read."""
     s = Step([64, 64], [1, 1], 8, 2, 128, 32, seed=15, spare_width=0)
-    ref = s.run()
-    s.lens = i32([64, 10 ** 9])
-    out = s.run()
-    assert torch.equal(out[0][0], ref[0][0])
+    for pad in (0, 2):
+        s.lens = i32([64, 64])
+        ref = s.run(pad=pad)
+        s.lens = i32([64, 10 ** 9])
+        out = s.run(pad=pad)
+        assert torch.equal(out[0][0], ref[0][0])
 
 
 def test_attention_on_another_stream_and_in_a_graph():
     s = Step([900, 33], [1, 1], 24, 4, 256, 64, seed=16)
-    ref = s.run()
+    ref = s.run(pad=0)
     side = torch.cuda.Stream()
     ws = torch.zeros(gdn.kv_attention_workspace_bytes(24, 4, 256), dtype=torch.uint8, device=DEV)
     out = torch.empty_like(s.q)
@@ -531,11 +540,11 @@ def test_attention_on_another_stream_and_in_a_graph():
     s.L = [800, 20]
     graph.replay()
     torch.cuda.synchronize()
-    assert torch.equal(out, s.run()[0])
+    assert torch.equal(out, s.run(pad=0)[0])
 
 
-@pytest.mark.parametrize("new", [1, 100])
-def test_attention_timeout_is_readable_and_recovers(new):
+@pytest.mark.parametrize("new,pad", [(1, 0), (100, 2)])
+def test_attention_timeout_is_readable_and_recovers(new, pad):
     """A wait limit of 0 makes the waits for copies just requested give up at their first
     empty probe (over a context whose copies cannot all have landed by the time they are
     waited for); the kernel still lets them land before it ends."""
@@ -543,12 +552,12 @@ def test_attention_timeout_is_readable_and_recovers(new):
     ws = torch.zeros(gdn.kv_attention_workspace_bytes(24, 4, 256), dtype=torch.uint8, device=DEV)
     prev = gdn.set_wait_limit_ns(0)
     try:
-        s.run(workspace=ws)
+        s.run(workspace=ws, pad=pad)
         assert gdn.kv_attention_status(ws) != 0
     finally:
         gdn.set_wait_limit_ns(prev)
     ws.zero_()
-    s.check(got=s.run(workspace=ws))
+    s.check(got=s.run(workspace=ws, pad=pad))
     assert gdn.kv_attention_status(ws) == 0
 
 
