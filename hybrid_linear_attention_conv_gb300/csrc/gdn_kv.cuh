@@ -121,16 +121,34 @@ __device__ __forceinline__ float2 float2_of_e4m3x2(uint32_t w) {
     return r;
 }
 
-// Four values as e4m3 hi + lo: hi = RNE(x), lo = RNE(x - hi).  x - hi is exact
-// in fp32; hi + lo holds eight significant bits of |x| >= 2^-2 and is within
-// 2^-10 of smaller ones (lo's smallest step is 2^-9).  So a bf16 value is held
-// exactly while it is within 2^-10 of its row's largest.
-__device__ __forceinline__ void split4_e4m3(const float (&x)[4], uint32_t& hi, uint32_t& lo) {
-    const uint32_t h0 = e4m3x2(x[0], x[1]), h1 = e4m3x2(x[2], x[3]);
-    const float2 f0 = float2_of_e4m3x2(h0), f1 = float2_of_e4m3x2(h1);
-    const uint32_t l0 = e4m3x2(x[0] - f0.x, x[1] - f0.y), l1 = e4m3x2(x[2] - f1.x, x[3] - f1.y);
-    hi = h0 | (h1 << 16);
-    lo = l0 | (l1 << 16);
+// Four values, |x| <= 448, as e4m3 hi + lo: hi = RNE(x), lo = RNE(x - hi), where
+// x - hi is exact.  hi + lo holds eight significant bits of |x| >= 2^-2 and is
+// within 2^-10 of smaller ones (lo's smallest step is 2^-9), so a bf16 value is
+// held exactly while it is within 2^-10 of its row's largest.  The values go by
+// way of f16 pairs, whose conversions are half the instructions: that rounds by
+// 2^-12 of x, and not at all where x has eleven significant bits or fewer.
+__device__ __forceinline__ uint32_t f16x2(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t w) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(w));
+    return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ void split4_f16(float e0, float e1, float e2, float e3, uint32_t& hi, uint32_t& lo) {
+    const uint32_t a = f16x2(e0, e1), b = f16x2(e2, e3);
+    const uint32_t ha = e4m3x2_of_f16x2(a), hb = e4m3x2_of_f16x2(b);
+    const uint32_t la = e4m3x2_of_f16x2(sub_f16x2(a, f16x2_of_e4m3x2(ha)));
+    const uint32_t lb = e4m3x2_of_f16x2(sub_f16x2(b, f16x2_of_e4m3x2(hb)));
+    hi = ha | (hb << 16);
+    lo = la | (lb << 16);
 }
 
 __device__ __forceinline__ float ex2(float x) {

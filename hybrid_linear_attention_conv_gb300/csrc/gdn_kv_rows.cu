@@ -269,9 +269,8 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_kv_attn_rows_kernel(const __g
                         f[2 * k] = finite ? __uint_as_float(u[k] << 16) * inv : 0.0f;
                         f[2 * k + 1] = finite ? __uint_as_float(u[k] & 0xffff0000u) * inv : 0.0f;
                     }
-                    const float lo4[4] = {f[0], f[1], f[2], f[3]}, hi4[4] = {f[4], f[5], f[6], f[7]};
-                    split4_e4m3(lo4, qa[hf * 4 + c][0], qa[hf * 4 + c][1]);
-                    split4_e4m3(hi4, qa[hf * 4 + c][2], qa[hf * 4 + c][3]);
+                    split4_f16(f[0], f[1], f[2], f[3], qa[hf * 4 + c][0], qa[hf * 4 + c][1]);
+                    split4_f16(f[4], f[5], f[6], f[7], qa[hf * 4 + c][2], qa[hf * 4 + c][3]);
                 }
         }
 
@@ -365,9 +364,8 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_kv_attn_rows_kernel(const __g
             if (sum != 0.0f) l = fmaf(sum, ex2(-lv), l);  // a row that sees nothing here takes nothing from the block's scale
             uint32_t pa[4];
             {
-                const float a[4] = {w[0], w[1], w[2], w[3]}, c[4] = {w[4], w[5], w[6], w[7]};
-                split4_e4m3(a, pa[0], pa[1]);
-                split4_e4m3(c, pa[2], pa[3]);
+                split4_f16(w[0], w[1], w[2], w[3], pa[0], pa[1]);
+                split4_f16(w[4], w[5], w[6], w[7], pa[2], pa[3]);
             }
             // ---- output
             wait_unit();

@@ -9,10 +9,12 @@
 // over both, twice the products at twice bf16's rate, with half its bytes
 // of operands and no conversion of a tile.
 //
-// Roles of the CTA's fourteen warps: one loads tiles (TMA) and their scales;
-// one thread issues the MMAs; eight are the softmax, in two halves of 64
-// columns, so that a tile's weights are ready within the time its neighbours'
-// MMAs take; four split the next item's q while the last tiles run.
+// Roles of the CTA's sixteen warps: one loads tiles (TMA) and their scales; one
+// thread issues the MMAs; eight are the softmax, in two halves of 64 columns,
+// so that a tile's weights are ready within the time its neighbours' MMAs take;
+// six split the next item's q, fetched into the L2 an item ahead, while the last
+// tiles run.  The softmax warps hold 64 logits a thread: the others give them
+// registers (88 and 168 of the 128 that the launch has for each).
 // Tensor memory: two tiles of logits (2 x 128 columns), over which their
 // weights are written as the second product's A operand, and the output
 // (d columns).  Per tile j the tensor pipe runs S(j + 1), then O += P(j) V(j).
@@ -35,7 +37,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kSoftWarps = 8, kQWarps = 4;
+constexpr int kSoftWarps = 8, kQWarps = 6;
 constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kQWarp0 = kSoftWarps + 2;
 constexpr int kThreads = (kSoftWarps + 2 + kQWarps) * 32;
 constexpr int kM = 128;                 // rows of an item
@@ -43,6 +45,7 @@ constexpr int kN = 128;                 // tokens of a tile
 constexpr float kPExp = 5.0f;           // weights are held times 2^5
 constexpr float kGrow = 3.8f;           // 2^(5 + 3.8) = 446
 constexpr int kScaleRing = 8;
+constexpr int kSoftRegs = 168, kOtherRegs = 88;  // 256 x (168 + 88) = 512 x 128
 constexpr int kMinTiles = 2;            // tiles a CTA takes at least
 constexpr uint64_t kDrainNs = 200000000ull;
 
@@ -55,6 +58,7 @@ struct TilesSmem {
     float4 scales[kScaleRing][2];                             // {key scale, log2 value scale} of 4 x 32 tokens
     float rf[kM];
     float red[2][2][kM];
+    alignas(16) uint8_t stage[kSoftWarps][32 * 64];           // a warp's 32 rows x 32 columns of output on their way out
     alignas(8) uint64_t full[kSlots], empty[kSlots], s_full[2], p_ready[2], scales_full[kScaleRing];
     uint64_t q_full, q_empty, o_done, o_free, drained;
     long long scan[kThreads / 32];
@@ -247,6 +251,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
     w.x = x0;
     w.x1 = x1;
 
+    // Inside the branches: code after a join of the two would have to fit the smaller number.
+    if (warp >= kSoftWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ tiles
         const int page_rows = min(1 << p.log2_page, kN), boxes = kN / page_rows;
@@ -367,55 +374,82 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
             tc::mbar_wait(drained, 0, kDrainNs);
         }
         __syncwarp();
-    } else if (warp >= kQWarp0) {
+    } else {
         // ----------------------------------------------------------- queries
         constexpr int kLanes = D / 16;              // of a row, 16 values each
         constexpr int kAtOnce = 32 / kLanes;        // rows of a warp's step
         const int sub = lane / kLanes, c = lane % kLanes;
+        constexpr int kBatch = 4;                   // steps whose loads go out together
         int item = 0;
-        for (; w.settle(p); w.advance(p), ++item) {
-            if (item > 0) wait(q_empty, item - 1);
-            const int rows = w.r.n * p.G;
-#pragma unroll 4
-            for (int i = 0; i < 32 / kAtOnce; ++i) {
-                const int local = (warp - kQWarp0) * 32 + i * kAtOnce + sub, row = w.t * kM + local;
-                uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-                if (row < rows) {
-                    const int qi = row / p.G, head = w.h * p.G + row - qi * p.G;
-                    const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(w.r.row0 + qi) * p.ldq + (int64_t)head * D) + 2 * c;
-                    x[0] = src[0];
-                    x[1] = src[1];
+        bool more = w.settle(p);
+        for (; more; ++item) {
+            const int rows = w.r.n * p.G - w.t * kM;  // of this item
+            bool waited = item == 0;
+#pragma unroll 1
+            for (int i0 = warp - kQWarp0; i0 < kM / kAtOnce; i0 += kBatch * kQWarps) {
+                uint4 x[kBatch][2];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int local = (i0 + i * kQWarps) * kAtOnce + sub;
+                    x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+                    if (local < min(rows, kM)) {
+                        const int row = w.t * kM + local, qi = row / p.G, head = w.h * p.G + row - qi * p.G;
+                        const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(w.r.row0 + qi) * p.ldq + (int64_t)head * D) + 2 * c;
+                        x[i][0] = src[0];
+                        x[i][1] = src[1];
+                    }
                 }
-                const uint32_t word[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
-                uint32_t m2 = 0;
+                if (!waited) wait(q_empty, item - 1);
+                waited = true;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) m2 = __vmaxu2(m2, word[k] & 0x7fff7fffu);
-                uint32_t top = max(m2 & 0xffffu, m2 >> 16);
+                for (int i = 0; i < kBatch; ++i) {
+                    const int local = (i0 + i * kQWarps) * kAtOnce + sub;
+                    if (i0 + i * kQWarps >= kM / kAtOnce) break;  // uniform in the warp
+                    const uint32_t word[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
+                    uint32_t m2 = 0;
 #pragma unroll
-                for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
-                const bool finite = top < 0x7f80u;
-                const int e = finite ? scale_exp_of_bf16(top) : 0;
-                const float inv = exp2_int(-e);
-                uint32_t hi[4], lo[4];
+                    for (int k = 0; k < 8; ++k) m2 = __vmaxu2(m2, word[k] & 0x7fff7fffu);
+                    uint32_t top = max(m2 & 0xffffu, m2 >> 16);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t a = finite ? word[2 * k] : 0u, b = finite ? word[2 * k + 1] : 0u;
-                    const float f[4] = {__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xffff0000u) * inv,
-                                        __uint_as_float(b << 16) * inv, __uint_as_float(b & 0xffff0000u) * inv};
-                    split4_e4m3(f, hi[k], lo[k]);
+                    for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+                    const bool finite = top < 0x7f80u;
+                    const int e = finite ? scale_exp_of_bf16(top) : 0;
+                    const float inv = exp2_int(-e);
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t a = finite ? word[2 * k] : 0u, b = finite ? word[2 * k + 1] : 0u;
+                        split4_f16(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xffff0000u) * inv, __uint_as_float(b << 16) * inv,
+                                   __uint_as_float(b & 0xffff0000u) * inv, hi[k], lo[k]);
+                    }
+                    const uint32_t at = (c >> 3) * (kM * 128) + local * 128 + (((c & 7) ^ (local & 7)) << 4);
+                    *reinterpret_cast<uint4*>(sm.q[0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(sm.q[1] + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    // a query that is not finite makes its row NaN, through the row's factor
+                    if (c == 0) sm.rf[local] = finite ? exp2_int(e) * p.scale_log2 : __int_as_float(0x7fffffff);
                 }
-                const uint32_t at = (c >> 3) * (kM * 128) + local * 128 + (((c & 7) ^ (local & 7)) << 4);
-                *reinterpret_cast<uint4*>(sm.q[0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(sm.q[1] + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                // a query that is not finite makes its row NaN, through the row's factor
-                if (c == 0) sm.rf[local] = finite ? exp2_int(e) * p.scale_log2 : __int_as_float(0x7fffffff);
             }
             tc::fence_async_smem();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(q_full);
+            w.advance(p);
+            more = w.settle(p);
+            if (more) {  // the next item's rows towards the L2 (a row is 2 or 4 lines)
+                const int rows_next = w.r.n * p.G;
+#pragma unroll 1
+                for (int i = (warp - kQWarp0) * 32 + lane; i < kM * (D / 64); i += kQWarps * 32) {
+                    const int row = w.t * kM + i / (D / 64);
+                    if (row < rows_next) {
+                        const int qi = row / p.G, head = w.h * p.G + row - qi * p.G;
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + (int64_t)(w.r.row0 + qi) * p.ldq + (int64_t)head * D + (i % (D / 64)) * 64));
+                    }
+                }
+            }
         }
+    }
     } else {
         // ----------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         const int quad = warp & 3, half = warp >> 2, local = quad * 32 + lane;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         int g = 0, item = 0;
@@ -442,22 +476,31 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                 tc::tmem_ld64(tmem + lanes + buf * 128 + half * 64, s);
                 float f0 = rf * sc.x, v0 = sc.y, f1 = rf * sc.z, v1 = sc.w;
                 if (j * kN + kN > all_see) {  // some row does not see some token: the logits themselves
+                    // the row's 64 tokens as bits: those below its limit, or below the tree and the nodes it sees
+                    auto below = [](int n) { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1; };
+                    const int first = base - pos0;  // column of the tree's first node
+                    unsigned long long vis = below(seen - pos0);
+                    if (p.tree != nullptr) {
+                        vis = below(first) | (first >= 64 || first <= -64 ? 0ull : first >= 0 ? tree << first : tree >> -first);
+                        vis = have ? vis & below(w.r.L - pos0) : 0ull;
+                    }
+                    const uint32_t vis0 = (uint32_t)vis, vis1 = (uint32_t)(vis >> 32);
 #pragma unroll
-                    for (int k = 0; k < 64; ++k) {
-                        const int pos = pos0 + k, node = pos - base;
-                        const bool vis = p.tree != nullptr ? have && pos < w.r.L && (node < 0 || (node < 64 && ((tree >> (node & 63)) & 1)))
-                                                           : pos < seen;
-                        s[k] = vis ? fmaf(s[k], k < 32 ? f0 : f1, k < 32 ? v0 : v1) : -INFINITY;
+                    for (int k = 0; k < 32; ++k) {
+                        s[k] = (vis0 >> k) & 1 ? fmaf(s[k], f0, v0) : -INFINITY;
+                        s[k + 32] = (vis1 >> k) & 1 ? fmaf(s[k + 32], f1, v1) : -INFINITY;
                     }
                     f0 = f1 = 1.0f;
                     v0 = v1 = 0.0f;
                 }
-                float top0 = s[0], top1 = s[32];
+                float t4[8];
 #pragma unroll
-                for (int k = 1; k < 32; ++k) {
-                    top0 = fmaxf(top0, s[k]);
-                    top1 = fmaxf(top1, s[k + 32]);
-                }
+                for (int k = 0; k < 8; ++k) t4[k] = fmaxf(fmaxf(s[8 * k], s[8 * k + 1]), s[8 * k + 2]);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) t4[k] = fmaxf(fmaxf(t4[k], s[8 * k + 3]), s[8 * k + 4]);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) t4[k] = fmaxf(fmaxf(t4[k], s[8 * k + 5]), fmaxf(s[8 * k + 6], s[8 * k + 7]));
+                const float top0 = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])), top1 = fmaxf(fmaxf(t4[4], t4[5]), fmaxf(t4[6], t4[7]));
                 float top = fmaxf(fmaf(top0, f0, v0), fmaf(top1, f1, v1));
                 sm.red[buf][half][local] = top;
                 tc::named_sync(1 + quad, 64);  // both halves have read their logits, too
@@ -483,17 +526,18 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                 }
                 const float shift = kPExp - (m == -INFINITY ? 0.0f : m);
                 const float a0 = v0 + shift, a1 = v1 + shift;
-                float sum0 = 0.0f, sum1 = 0.0f;
+                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
                     const float f = k < 8 ? f0 : f1, a = k < 8 ? a0 : a1;
-                    const float e[4] = {ex2(fmaf(s[4 * k], f, a)), ex2(fmaf(s[4 * k + 1], f, a)), ex2(fmaf(s[4 * k + 2], f, a)),
-                                        ex2(fmaf(s[4 * k + 3], f, a))};
-                    if (k < 8) sum0 += (e[0] + e[1]) + (e[2] + e[3]);
-                    else sum1 += (e[0] + e[1]) + (e[2] + e[3]);
-                    split4_e4m3(e, hi[k], lo[k]);
+                    const float e0 = ex2(fmaf(s[4 * k], f, a)), e1 = ex2(fmaf(s[4 * k + 1], f, a)), e2 = ex2(fmaf(s[4 * k + 2], f, a)),
+                                e3 = ex2(fmaf(s[4 * k + 3], f, a));
+                    part[k < 8 ? 0 : 2] += e0 + e1;
+                    part[k < 8 ? 1 : 3] += e2 + e3;
+                    split4_f16(e0, e1, e2, e3, hi[k], lo[k]);
                 }
+                const float sum0 = part[0] + part[1], sum1 = part[2] + part[3];
                 tc::tmem_st16(tmem + lanes + buf * 128 + half * 16, hi);
                 tc::tmem_st16(tmem + lanes + buf * 128 + 32 + half * 16, lo);
                 if (sum0 != 0.0f) l = fmaf(sum0, ex2(-sc.y), l);  // a row that sees nothing here takes nothing from the block's scale
@@ -522,16 +566,30 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
             const long long item0 = w.x - w.j0;
             const int c0 = (int)(item0 / W), c1 = (int)((item0 + w.kt - 1) / W);
             const int64_t at = (int64_t)(w.r.row0 + qi) * p.Hq + head;
-            auto put = [&](int k, const float (&o)[32], float inv) {  // columns half * D / 2 + 32 k ..
-                if (!have) return;
-                uint16_t* dst = p.out + at * D + half * (D / 2) + 32 * k;
+            // 32 columns from half * D / 2 + 32 k of the warp's 32 rows, through shared
+            // memory: a row's 64 bytes then leave from four lanes (a thread storing its own row
+            // would touch 32 lines with every instruction).
+            const int rows_here = min(kM, w.r.n * p.G - w.t * kM);
+            auto put = [&](int k, const float (&o)[32], float inv) {
+                uint4* stage = reinterpret_cast<uint4*>(sm.stage[warp]);
+                __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t u[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         u[e] = tc::pack_bf16(__float2bfloat16_rn(o[8 * i + 2 * e] * inv), __float2bfloat16_rn(o[8 * i + 2 * e + 1] * inv));
-                    reinterpret_cast<uint4*>(dst)[i] = make_uint4(u[0], u[1], u[2], u[3]);
+                    stage[lane * 4 + (i ^ ((lane >> 1) & 3))] = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = i * 8 + (lane >> 2), out_row = w.t * kM + quad * 32 + r;
+                    if (quad * 32 + r < rows_here) {
+                        const int oq = out_row / p.G, oh = w.h * p.G + out_row - oq * p.G;
+                        uint4* dst = reinterpret_cast<uint4*>(p.out + ((int64_t)(w.r.row0 + oq) * p.Hq + oh) * D + half * (D / 2) + 32 * k);
+                        dst[lane & 3] = stage[r * 4 + ((lane & 3) ^ ((r >> 1) & 3))];
+                    }
                 }
             };
             auto put_lse = [&]() {
