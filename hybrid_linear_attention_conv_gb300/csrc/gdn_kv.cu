@@ -566,6 +566,7 @@ int gdn_kv_attention(const gdn_kv_shape* shape, int32_t T, const gdn_bf16* q, in
     p.pages = shape->pages;
     p.log2_page = log2_of(shape->page);
     p.scale_log2 = scale * 1.4426950408889634f;
+    p.group_magic = ((1u << 22) + p.G - 1) / p.G;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = tiles ? launch_kv_attn_tiles(p, shape->d, st) : launch_kv_attn_rows(p, shape->d, st);
     return e == cudaSuccess ? GDN_OK : cuda_error(e, "cache attention launch");

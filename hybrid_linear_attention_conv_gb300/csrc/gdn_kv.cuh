@@ -81,6 +81,7 @@ struct KvAttnParams {
     int64_t ldq;
     int T, B, Hq, Hkv, G, width, pages, log2_page;
     float scale_log2;           // scale * log2(e)
+    unsigned group_magic;       // ceil(2^22 / G)
 };
 
 // Workspace: 256 bytes of status, the counters, then the partial results.

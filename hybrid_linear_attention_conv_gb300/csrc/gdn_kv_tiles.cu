@@ -10,11 +10,10 @@
 // of operands and no conversion of a tile.
 //
 // Roles of the CTA's sixteen warps: one loads tiles (TMA) and their scales; one
-// thread issues the MMAs; eight are the softmax, in two halves of 64 columns,
-// so that a tile's weights are ready within the time its neighbours' MMAs take;
-// six split the next item's q, fetched into the L2 an item ahead, while the last
-// tiles run.  The softmax warps hold 64 logits a thread: the others give them
-// registers (88 and 168 of the 128 that the launch has for each).
+// thread issues the MMAs; eight are the softmax, in two teams that take turns
+// at the tiles; six split the next item's q, fetched into the L2 an item ahead,
+// while the last tiles run.  The softmax warps hold 64 logits a thread: the
+// others give them registers (88 and 168 of the 128 that the launch has for each).
 // Tensor memory: two tiles of logits (2 x 128 columns), over which their
 // weights are written as the second product's A operand, and the output
 // (d columns).  Per tile j the tensor pipe runs S(j + 1), then O += P(j) V(j).
@@ -57,10 +56,11 @@ struct TilesSmem {
     alignas(1024) uint8_t ring[kSlots][kSlot];
     float4 scales[kScaleRing][2];                             // {key scale, log2 value scale} of 4 x 32 tokens
     float rf[kM];
-    float red[2][2][kM];
+    float ref[2][kM];                                         // the rows' references after each team's last tile
+    float ml[2][2][2][kM];                                    // by item: each team's reference and sum
     alignas(16) uint8_t stage[kSoftWarps][32 * 64];           // a warp's 32 rows x 32 columns of output on their way out
-    alignas(8) uint64_t full[kSlots], empty[kSlots], s_full[2], p_ready[2], scales_full[kScaleRing];
-    uint64_t q_full, q_empty, o_done, o_free, drained;
+    alignas(8) uint64_t full[kSlots], empty[kSlots], s_full[2], p_ready[2], o_done[2], scales_full[kScaleRing];
+    uint64_t q_full, q_empty, item_done, o_free, drained;
     long long scan[kThreads / 32];
     int qbase[kThreads];
     int at_b, at_t, at_h, at_j;
@@ -114,6 +114,24 @@ struct Walk {
             h = 0;
             ++t;
         }
+    }
+};
+
+// Rows of an item -> query and head of the group, without a division for each:
+// local + rem < G + 128 <= 1152, and x * ceil(2^22 / G) >> 22 is x / G there.
+struct RowMap {
+    int G, q0, rem;
+    unsigned magic;
+    __device__ __forceinline__ RowMap(const KvAttnParams& p, int t) {
+        G = p.G;
+        q0 = t * kM / G;
+        rem = t * kM - q0 * G;
+        magic = p.group_magic;
+    }
+    __device__ __forceinline__ void find(int local, int& q, int& h) const {
+        const int x = rem + local, d = (int)(((unsigned)x * magic) >> 22);
+        q = q0 + d;
+        h = x - d * G;
     }
 };
 
@@ -207,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
     const uint32_t full = tc::smem_u32(sm.full), empty = tc::smem_u32(sm.empty), s_full = tc::smem_u32(sm.s_full),
                    p_ready = tc::smem_u32(sm.p_ready), scales_full = tc::smem_u32(sm.scales_full),
                    q_full = tc::smem_u32(&sm.q_full), q_empty = tc::smem_u32(&sm.q_empty),
-                   o_done = tc::smem_u32(&sm.o_done), o_free = tc::smem_u32(&sm.o_free),
+                   o_done = tc::smem_u32(sm.o_done), o_free = tc::smem_u32(&sm.o_free), item_done = tc::smem_u32(&sm.item_done),
                    drained = tc::smem_u32(&sm.drained);
     if (tid == 0) {
         sm.dead = 0;
@@ -217,13 +235,14 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(s_full + 8 * i, 1);
-            tc::mbar_init(p_ready + 8 * i, kSoftWarps);
+            tc::mbar_init(o_done + 8 * i, 1);
+            tc::mbar_init(p_ready + 8 * i, kSoftWarps / 2);
         }
         for (int i = 0; i < kScaleRing; ++i) tc::mbar_init(scales_full + 8 * i, 1);
         tc::mbar_init(q_full, kQWarps);
         tc::mbar_init(q_empty, 1 + kSoftWarps);
-        tc::mbar_init(o_done, 1);
         tc::mbar_init(o_free, kSoftWarps);
+        tc::mbar_init(item_done, 1);
         tc::mbar_init(drained, 1);
     }
     if (warp == kMmaWarp) tc::tmem_alloc(tc::smem_u32(&sm.tmem), 512);
@@ -243,6 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
         }
     };
 
+    const int n_tiles = (int)(x1 - x0);
     Walk w;
     w.b = sm.at_b;
     w.t = sm.at_t;
@@ -314,66 +334,76 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                 for (uint32_t par = 0; par < 2; ++par) tc::mbar_wait(full + 8 * i, par, kDrainNs / 20);
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------- MMAs
-        if (lane == 0) {
-            constexpr uint32_t id_s = tc::idesc_e4m3(kM, kN, false), id_o = tc::idesc_e4m3(kM, D, true);
-            const uint32_t q_hi = tc::smem_u32(sm.q[0]), q_lo = tc::smem_u32(sm.q[1]);
-            int g = 0, item = 0;
-            bool pending = false, pend_first = false;  // the weights' product of tile g - 1
-            int pend_item = 0;
-            auto product = [&]() {
-                if (!pending) return;
-                pending = false;
-                const int gp = g - 1, u = 2 * gp + 1, slot = u % kSlots, buf = gp & 1;
-                if (pend_first && pend_item > 0) wait(o_free, pend_item - 1);
-                wait(full + 8 * slot, u / kSlots);
-                wait(p_ready + 8 * buf, gp >> 1);
-                if (*dead) return;
-                tc::fence_after_sync();
-                const uint32_t v = tc::smem_u32(sm.ring[slot]), a = tmem + buf * 128;
+        // The whole warp walks and waits; one elected lane issues.  (An MMA takes
+        // its descriptors from uniform registers: under a test of the lane number
+        // instead, each one costs about 185 cycles of issue, three times its own 64.)
+        constexpr uint32_t id_s = tc::idesc_e4m3(kM, kN, false), id_o = tc::idesc_e4m3(kM, D, true);
+        const uint64_t q_hi = tc::smem_desc_sw128(tc::smem_u32(sm.q[0])), q_lo = tc::smem_desc_sw128(tc::smem_u32(sm.q[1]));
+        const uint32_t ring = tc::smem_u32(sm.ring[0]);
+        int g = 0, item = 0;
+        bool pending = false, pend_first = false, pend_last = false;  // the weights' product of tile g - 1
+        int pend_item = 0;
+        auto product = [&]() {
+            if (!pending) return;
+            pending = false;
+            const int gp = g - 1, u = 2 * gp + 1, slot = u % kSlots, buf = gp & 1;
+            if (pend_first && pend_item > 0) wait(o_free, pend_item - 1);
+            wait(full + 8 * slot, u / kSlots);
+            wait(p_ready + 8 * buf, gp >> 1);
+            if (*dead) return;
+            tc::fence_after_sync();
+            const uint64_t v = tc::smem_desc_mn_sw128(ring + slot * kSlot, kHalfBytes);
+            const uint32_t a = tmem + buf * 128;
+            if (tc::elect_one()) {
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int ks = 0; ks < kN / 32; ++ks)
-                        tc::mma_e4m3_ts(tO, a + part * 32 + ks * 8, tc::smem_desc_mn_sw128(v + ks * 32 * 128, kHalfBytes), id_o,
-                                        !(pend_first && part == 0 && ks == 0));
+                        tc::mma_e4m3_ts(tO, a + part * 32 + ks * 8, v + (ks * 32 * 128 >> 4), id_o, part + ks > 0 || !pend_first);
                 tc::mma_commit(empty + 8 * slot);
-                tc::mma_commit(o_done);
-            };
-            for (; w.settle(p); w.advance(p), ++item) {
-                // the last item's product first, unless this item's q is there already
-                if (!tc::mbar_test(q_full, item & 1)) product();
-                wait(q_full, item);
-                for (int j = w.j0; j < w.j1; ++j) {
-                    const int u = 2 * g, slot = u % kSlots, buf = g & 1;
-                    wait(full + 8 * slot, u / kSlots);
-                    if (!*dead) {
-                        tc::fence_after_sync();
-                        const uint32_t k = tc::smem_u32(sm.ring[slot]);
+                tc::mma_commit(o_done + 8 * buf);
+                if (pend_last) tc::mma_commit(item_done);
+            }
+            __syncwarp();
+        };
+        for (; w.settle(p); w.advance(p), ++item) {
+            // the last item's product first, unless this item's q is there already
+            if (!__all_sync(~0u, tc::mbar_test(q_full, item & 1))) product();
+            wait(q_full, item);
+            for (int j = w.j0; j < w.j1; ++j) {
+                const int u = 2 * g, slot = u % kSlots, buf = g & 1;
+                wait(full + 8 * slot, u / kSlots);
+                if (!*dead) {
+                    tc::fence_after_sync();
+                    const uint64_t k = tc::smem_desc_sw128(ring + slot * kSlot);
+                    const uint32_t d = tmem + buf * 128;
+                    if (tc::elect_one()) {
 #pragma unroll
                         for (int part = 0; part < 2; ++part)
 #pragma unroll
                             for (int ks = 0; ks < D / 32; ++ks) {
-                                const uint32_t at = (ks >> 2) * kHalfBytes + (ks & 3) * 32;
-                                tc::mma_e4m3(tmem + buf * 128, tc::smem_desc_sw128((part ? q_lo : q_hi) + at), tc::smem_desc_sw128(k + at),
-                                             id_s, part + ks > 0);
+                                const uint32_t at = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
+                                tc::mma_e4m3(d, (part ? q_lo : q_hi) + at, k + at, id_s, part + ks > 0);
                             }
                         tc::mma_commit(empty + 8 * slot);
                         tc::mma_commit(s_full + 8 * buf);
                         if (j == w.j1 - 1) tc::mma_commit(q_empty);
                     }
-                    product();
-                    ++g;
-                    pending = true;
-                    pend_first = j == w.j0;
-                    pend_item = item;
+                    __syncwarp();
                 }
+                product();
+                ++g;
+                pending = true;
+                pend_first = j == w.j0;
+                pend_last = j == w.j1 - 1;
+                pend_item = item;
             }
-            product();
-            // every MMA has ended before tensor memory is given back
-            tc::mma_commit(drained);
-            tc::mbar_wait(drained, 0, kDrainNs);
         }
+        product();
+        // every MMA has ended before tensor memory is given back
+        if (tc::elect_one()) tc::mma_commit(drained);
         __syncwarp();
+        tc::mbar_wait(drained, 0, kDrainNs);
     } else {
         // ----------------------------------------------------------- queries
         constexpr int kLanes = D / 16;              // of a row, 16 values each
@@ -384,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
         bool more = w.settle(p);
         for (; more; ++item) {
             const int rows = w.r.n * p.G - w.t * kM;  // of this item
+            const RowMap map(p, w.t);
             bool waited = item == 0;
 #pragma unroll 1
             for (int i0 = warp - kQWarp0; i0 < kM / kAtOnce; i0 += kBatch * kQWarps) {
@@ -393,8 +424,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                     const int local = (i0 + i * kQWarps) * kAtOnce + sub;
                     x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
                     if (local < min(rows, kM)) {
-                        const int row = w.t * kM + local, qi = row / p.G, head = w.h * p.G + row - qi * p.G;
-                        const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(w.r.row0 + qi) * p.ldq + (int64_t)head * D) + 2 * c;
+                        int qi, hg;
+                        map.find(local, qi, hg);
+                        const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(w.r.row0 + qi) * p.ldq + (int64_t)(w.h * p.G + hg) * D) + 2 * c;
                         x[i][0] = src[0];
                         x[i][1] = src[1];
                     }
@@ -435,13 +467,15 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
             w.advance(p);
             more = w.settle(p);
             if (more) {  // the next item's rows towards the L2 (a row is 2 or 4 lines)
-                const int rows_next = w.r.n * p.G;
+                const int rows_next = w.r.n * p.G - w.t * kM;
+                const RowMap map_next(p, w.t);
 #pragma unroll 1
                 for (int i = (warp - kQWarp0) * 32 + lane; i < kM * (D / 64); i += kQWarps * 32) {
-                    const int row = w.t * kM + i / (D / 64);
-                    if (row < rows_next) {
-                        const int qi = row / p.G, head = w.h * p.G + row - qi * p.G;
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + (int64_t)(w.r.row0 + qi) * p.ldq + (int64_t)head * D + (i % (D / 64)) * 64));
+                    const int local = i / (D / 64);
+                    if (local < rows_next) {
+                        int qi, hg;
+                        map_next.find(local, qi, hg);
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + (int64_t)(w.r.row0 + qi) * p.ldq + (int64_t)(w.h * p.G + hg) * D + (i % (D / 64)) * 64));
                     }
                 }
             }
@@ -449,124 +483,172 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
     }
     } else {
         // ----------------------------------------------------------- softmax
+        // Team 0 has the even tiles of the CTA, team 1 the odd ones, a thread a
+        // row: one team's exponentials run while the other reads its logits.
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-        const int quad = warp & 3, half = warp >> 2, local = quad * 32 + lane;
-        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        const int quad = warp & 3, team = warp >> 2, local = quad * 32 + lane;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16, tS = tmem + lanes + team * 128;
         int g = 0, item = 0;
         for (; w.settle(p); w.advance(p), ++item) {
+            const RowMap rows(p, w.t);
             const int row = w.t * kM + local;
             const bool have = row < w.r.n * p.G;
-            const int qi = have ? row / p.G : 0, head = w.h * p.G + (have ? row - qi * p.G : 0);
+            int qi, hg;
+            rows.find(local, qi, hg);
+            if (!have) qi = hg = 0;
+            const int64_t at = (int64_t)(w.r.row0 + qi) * p.Hq + w.h * p.G + hg;
             const int base = w.r.L - w.r.n;
             const int seen = have ? base + qi + 1 : 0;
             const unsigned long long tree = p.tree != nullptr && have ? (unsigned long long)p.tree[w.r.row0 + qi] : 0ull;
-            const int all_see = max(0, min(w.r.L, p.tree != nullptr ? base : base + (w.t * kM) / p.G + 1));
+            const int all_see = max(0, min(w.r.L, p.tree != nullptr ? base : base + rows.q0 + 1));
             wait(q_full, item);
             const float rf = sm.rf[local];
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(q_empty);
-            float m = -INFINITY, l = 0.0f;
+            float m = -INFINITY, l = 0.0f;  // l: this team's tiles', relative to m
             for (int j = w.j0; j < w.j1; ++j, ++g) {
-                const int buf = g & 1, pos0 = j * kN + half * 64;
+                if ((g & 1) != team) continue;
                 wait(scales_full + 8 * (g % kScaleRing), g / kScaleRing);
-                const float4 sc = sm.scales[g % kScaleRing][half];  // two stretches of 32 tokens
-                wait(s_full + 8 * buf, g >> 1);
-                tc::fence_after_sync();
-                float s[64];
-                tc::tmem_ld64(tmem + lanes + buf * 128 + half * 64, s);
-                float f0 = rf * sc.x, v0 = sc.y, f1 = rf * sc.z, v1 = sc.w;
-                if (j * kN + kN > all_see) {  // some row does not see some token: the logits themselves
-                    // the row's 64 tokens as bits: those below its limit, or below the tree and the nodes it sees
+                const float4 sc[2] = {sm.scales[g % kScaleRing][0], sm.scales[g % kScaleRing][1]};  // four stretches of 32 tokens
+                const float f[4] = {rf * sc[0].x, rf * sc[0].z, rf * sc[1].x, rf * sc[1].z};
+                const float v[4] = {sc[0].y, sc[0].w, sc[1].y, sc[1].w};
+                // the row's 128 tokens as bits: those below its limit, or below the tree and the nodes it sees
+                const bool masked = j * kN + kN > all_see;
+                uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+                if (masked) {
                     auto below = [](int n) { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1; };
-                    const int first = base - pos0;  // column of the tree's first node
-                    unsigned long long vis = below(seen - pos0);
-                    if (p.tree != nullptr) {
-                        vis = below(first) | (first >= 64 || first <= -64 ? 0ull : first >= 0 ? tree << first : tree >> -first);
-                        vis = have ? vis & below(w.r.L - pos0) : 0ull;
-                    }
-                    const uint32_t vis0 = (uint32_t)vis, vis1 = (uint32_t)(vis >> 32);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        s[k] = (vis0 >> k) & 1 ? fmaf(s[k], f0, v0) : -INFINITY;
-                        s[k + 32] = (vis1 >> k) & 1 ? fmaf(s[k + 32], f1, v1) : -INFINITY;
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const int pos0 = j * kN + hf * 64, first = base - pos0;  // column of the tree's first node
+                        unsigned long long bits = below(seen - pos0);
+                        if (p.tree != nullptr) {
+                            bits = below(first) | (first >= 64 || first <= -64 ? 0ull : first >= 0 ? tree << first : tree >> -first);
+                            bits = have ? bits & below(w.r.L - pos0) : 0ull;
+                        }
+                        vis[2 * hf] = (uint32_t)bits;
+                        vis[2 * hf + 1] = (uint32_t)(bits >> 32);
                     }
-                    f0 = f1 = 1.0f;
-                    v0 = v1 = 0.0f;
                 }
-                float t4[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) t4[k] = fmaxf(fmaxf(s[8 * k], s[8 * k + 1]), s[8 * k + 2]);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) t4[k] = fmaxf(fmaxf(t4[k], s[8 * k + 3]), s[8 * k + 4]);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) t4[k] = fmaxf(fmaxf(t4[k], s[8 * k + 5]), fmaxf(s[8 * k + 6], s[8 * k + 7]));
-                const float top0 = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])), top1 = fmaxf(fmaxf(t4[4], t4[5]), fmaxf(t4[6], t4[7]));
-                float top = fmaxf(fmaf(top0, f0, v0), fmaf(top1, f1, v1));
-                sm.red[buf][half][local] = top;
-                tc::named_sync(1 + quad, 64);  // both halves have read their logits, too
-                top = fmaxf(top, sm.red[buf][half ^ 1][local]);
-                const bool grows = m > -INFINITY && top > m + kGrow;
-                if (m == -INFINITY) m = fmaxf(m, top);
-                if (__any_sync(~0u, grows)) {
-                    const float c = grows ? ex2(m - top) : 1.0f;
-                    if (grows) m = top;
-                    l *= c;
-                    if (j > w.j0) {
-                        wait(o_done, g - 1);
-                        tc::fence_after_sync();
+                wait(s_full + 8 * team, g >> 1);
+                tc::fence_after_sync();
+
+                // ---- the tile's maximum (the second half first: the first one's logits stay in registers)
+                float s[64], top = -INFINITY;
 #pragma unroll 1
-                        for (int k = 0; k < D / 64; ++k) {
-                            float o[32];
-                            tc::tmem_ld32(tO + lanes + half * (D / 2) + 32 * k, o);
+                for (int hf = 1; hf >= 0; --hf) {
+                    tc::tmem_ld64(tS + hf * 64, s);
+                    const uint32_t vis0 = hf ? vis[2] : vis[0], vis1 = hf ? vis[3] : vis[1];
+                    if (masked) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] *= c;
-                            tc::tmem_st32(tO + lanes + half * (D / 2) + 32 * k, o);
+                        for (int k = 0; k < 32; ++k) {
+                            s[k] = (vis0 >> k) & 1 ? s[k] : -INFINITY;
+                            s[k + 32] = (vis1 >> k) & 1 ? s[k + 32] : -INFINITY;
                         }
                     }
-                }
-                const float shift = kPExp - (m == -INFINITY ? 0.0f : m);
-                const float a0 = v0 + shift, a1 = v1 + shift;
-                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                uint32_t hi[16], lo[16];
+                    float t8[8];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const float f = k < 8 ? f0 : f1, a = k < 8 ? a0 : a1;
-                    const float e0 = ex2(fmaf(s[4 * k], f, a)), e1 = ex2(fmaf(s[4 * k + 1], f, a)), e2 = ex2(fmaf(s[4 * k + 2], f, a)),
-                                e3 = ex2(fmaf(s[4 * k + 3], f, a));
-                    part[k < 8 ? 0 : 2] += e0 + e1;
-                    part[k < 8 ? 1 : 3] += e2 + e3;
-                    split4_f16(e0, e1, e2, e3, hi[k], lo[k]);
+                    for (int k = 0; k < 8; ++k) t8[k] = fmaxf(fmaxf(s[8 * k], s[8 * k + 1]), s[8 * k + 2]);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) t8[k] = fmaxf(fmaxf(t8[k], s[8 * k + 3]), s[8 * k + 4]);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) t8[k] = fmaxf(fmaxf(t8[k], s[8 * k + 5]), fmaxf(s[8 * k + 6], s[8 * k + 7]));
+                    const float top0 = fmaxf(fmaxf(t8[0], t8[1]), fmaxf(t8[2], t8[3])), top1 = fmaxf(fmaxf(t8[4], t8[5]), fmaxf(t8[6], t8[7]));
+                    top = fmaxf(top, fmaxf(fmaf(top0, hf ? f[2] : f[0], hf ? v[2] : v[0]), fmaf(top1, hf ? f[3] : f[1], hf ? v[3] : v[1])));
                 }
-                const float sum0 = part[0] + part[1], sum1 = part[2] + part[3];
-                tc::tmem_st16(tmem + lanes + buf * 128 + half * 16, hi);
-                tc::tmem_st16(tmem + lanes + buf * 128 + 32 + half * 16, lo);
-                if (sum0 != 0.0f) l = fmaf(sum0, ex2(-sc.y), l);  // a row that sees nothing here takes nothing from the block's scale
-                if (sum1 != 0.0f) l = fmaf(sum1, ex2(-sc.w), l);
+
+                // ---- the reference: the other team's after the tile before, raised where this tile asks for it
+                if (g > 0) tc::named_sync(1 + 4 * team + quad, 64);
+                float ref = j > w.j0 ? sm.ref[team ^ 1][local] : -INFINITY;
+                const bool grows = ref > -INFINITY && top > ref + kGrow;
+                const float c = grows ? ex2(ref - top) : 1.0f;
+                if (ref == -INFINITY || grows) ref = fmaxf(ref, top);
+                sm.ref[team][local] = ref;
+                if (g + 1 < n_tiles) tc::named_arrive(1 + 4 * (team ^ 1) + quad, 64);
+                l *= factor(m, ref);
+                m = ref;
+                if (j > w.j0 && __any_sync(~0u, grows)) {
+                    // This tile's logits came after product g - 2, and product g waits for this team: the barrier
+                    // is in the phase of product g - 1 or just past it, which its parity tells apart.
+                    wait(o_done + 8 * (team ^ 1), (g - 1) >> 1);
+                    tc::fence_after_sync();
+#pragma unroll 1
+                    for (int k = 0; k < D / 32; ++k) {
+                        float o[32];
+                        tc::tmem_ld32(tO + lanes + 32 * k, o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] *= c;
+                        tc::tmem_st32(tO + lanes + 32 * k, o);
+                    }
+                }
+
+                // ---- weights
+                const float shift = kPExp - (m == -INFINITY ? 0.0f : m);
+#pragma unroll 1
+                for (int hf = 0; hf < 2; ++hf) {
+                    if (hf) tc::tmem_ld64(tS + 64, s);
+                    const float f0 = hf ? f[2] : f[0], f1 = hf ? f[3] : f[1], v0 = hf ? v[2] : v[0], v1 = hf ? v[3] : v[1];
+                    const float a0 = v0 + shift, a1 = v1 + shift;
+                    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    uint32_t hi[16], lo[16];
+                    if (!masked) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const float ff = k < 8 ? f0 : f1, a = k < 8 ? a0 : a1;
+                            const float e0 = ex2(fmaf(s[4 * k], ff, a)), e1 = ex2(fmaf(s[4 * k + 1], ff, a)),
+                                        e2 = ex2(fmaf(s[4 * k + 2], ff, a)), e3 = ex2(fmaf(s[4 * k + 3], ff, a));
+                            part[k < 8 ? 0 : 2] += e0 + e1;
+                            part[k < 8 ? 1 : 3] += e2 + e3;
+                            split4_f16(e0, e1, e2, e3, hi[k], lo[k]);
+                        }
+                    } else {
+                        const uint32_t vis0 = hf ? vis[2] : vis[0], vis1 = hf ? vis[3] : vis[1];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const float ff = k < 8 ? f0 : f1, a = k < 8 ? a0 : a1;
+                            const uint32_t bits = (k < 8 ? vis0 : vis1) >> (4 * (k & 7));
+                            float e[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) e[i] = (bits >> i) & 1 ? ex2(fmaf(s[4 * k + i], ff, a)) : 0.0f;
+                            part[k < 8 ? 0 : 2] += e[0] + e[1];
+                            part[k < 8 ? 1 : 3] += e[2] + e[3];
+                            split4_f16(e[0], e[1], e[2], e[3], hi[k], lo[k]);
+                        }
+                    }
+                    tc::tmem_st16(tS + hf * 16, hi);
+                    tc::tmem_st16(tS + 32 + hf * 16, lo);
+                    // a row that sees nothing here takes nothing from the block's scale
+                    if (part[0] + part[1] != 0.0f) l = fmaf(part[0] + part[1], ex2(-v0), l);
+                    if (part[2] + part[3] != 0.0f) l = fmaf(part[2] + part[3], ex2(-v1), l);
+                }
                 if (j * kN + kN > w.r.L) {  // whatever lies past the end: zeros for the product
                     const int u = 2 * g + 1, slot = u % kSlots;
                     wait(full + 8 * slot, u / kSlots);
                     const int first = max(0, w.r.L - j * kN);
-                    for (int i = tid; i < (kN - first) * (D / 16); i += kSoftWarps * 32) {
-                        const int tok = first + i / (D / 16), c = i % (D / 16);
-                        *reinterpret_cast<uint4*>(sm.ring[slot] + (c >> 3) * kHalfBytes + tok * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    for (int i = local; i < (kN - first) * (D / 16); i += kM) {
+                        const int tok = first + i / (D / 16), cc = i % (D / 16);
+                        *reinterpret_cast<uint4*>(sm.ring[slot] + (cc >> 3) * kHalfBytes + tok * 128 + (cc & 7) * 16) = make_uint4(0, 0, 0, 0);
                     }
                     tc::fence_async_smem();
                 }
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(p_ready + 8 * buf);
+                if (lane == 0) tc::mbar_arrive(p_ready + 8 * team);
             }
 
-            // ---- the item's output: whole, or this CTA's part of it
-            sm.red[g & 1][half][local] = l;
-            tc::named_sync(1 + quad, 64);
-            l += sm.red[g & 1][half ^ 1][local];
-            tc::named_sync(1 + quad, 64);  // read before the next item writes there
+            // ---- the item's output: whole, or this CTA's part of it.  Each team has half the columns.
+            sm.ml[item & 1][team][0][local] = m;
+            sm.ml[item & 1][team][1][local] = l;
+            tc::named_sync(9 + quad, 64);
+            {
+                const float m0 = sm.ml[item & 1][0][0][local], m1 = sm.ml[item & 1][1][0][local];
+                // the last tile's team has the final reference; O is relative to it
+                m = ((g - 1) & 1) == 0 ? m0 : m1;
+                l = sm.ml[item & 1][0][1][local] * factor(m0, m) + sm.ml[item & 1][1][1][local] * factor(m1, m);
+            }
             const long long item0 = w.x - w.j0;
             const int c0 = (int)(item0 / W), c1 = (int)((item0 + w.kt - 1) / W);
-            const int64_t at = (int64_t)(w.r.row0 + qi) * p.Hq + head;
-            // 32 columns from half * D / 2 + 32 k of the warp's 32 rows, through shared
+            // 32 columns from team * D / 2 + 32 k of the warp's 32 rows, through shared
             // memory: a row's 64 bytes then leave from four lanes (a thread storing its own row
             // would touch 32 lines with every instruction).
             const int rows_here = min(kM, w.r.n * p.G - w.t * kM);
@@ -584,26 +666,24 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int r = i * 8 + (lane >> 2), out_row = w.t * kM + quad * 32 + r;
-                    if (quad * 32 + r < rows_here) {
-                        const int oq = out_row / p.G, oh = w.h * p.G + out_row - oq * p.G;
-                        uint4* dst = reinterpret_cast<uint4*>(p.out + ((int64_t)(w.r.row0 + oq) * p.Hq + oh) * D + half * (D / 2) + 32 * k);
-                        dst[lane & 3] = stage[r * 4 + ((lane & 3) ^ ((r >> 1) & 3))];
-                    }
+                    const int r = i * 8 + (lane >> 2);
+                    const int64_t to = __shfl_sync(~0u, at, r);
+                    if (quad * 32 + r < rows_here)
+                        reinterpret_cast<uint4*>(p.out + to * D + team * (D / 2) + 32 * k)[lane & 3] = stage[r * 4 + ((lane & 3) ^ ((r >> 1) & 3))];
                 }
             };
             auto put_lse = [&]() {
-                if (p.lse != nullptr && have && half == 0)
+                if (p.lse != nullptr && have && team == 0)
                     p.lse[at] = l == 0.0f ? -INFINITY : ((m == -INFINITY ? 0.0f : m) - kPExp + log2f(l)) * 0.69314718055994531f;
             };
-            wait(o_done, g - 1);
+            wait(item_done, item);
             tc::fence_after_sync();
             if (c0 == c1) {
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no token seen: zeros
 #pragma unroll 1
                 for (int k = 0; k < D / 64; ++k) {
                     float o[32];
-                    tc::tmem_ld32(tO + lanes + half * (D / 2) + 32 * k, o);
+                    tc::tmem_ld32(tO + lanes + team * (D / 2) + 32 * k, o);
                     put(k, o, inv);
                 }
                 put_lse();
@@ -612,13 +692,13 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
 #pragma unroll 1
                 for (int k = 0; k < D / 64; ++k) {
                     float o[32];
-                    tc::tmem_ld32(tO + lanes + half * (D / 2) + 32 * k, o);
+                    tc::tmem_ld32(tO + lanes + team * (D / 2) + 32 * k, o);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        reinterpret_cast<float4*>(part)[(half * (D / 8) + 8 * k + i) * kM + local] =
+                        reinterpret_cast<float4*>(part)[(team * (D / 8) + 8 * k + i) * kM + local] =
                             make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                 }
-                if (half == 0) {
+                if (team == 0) {
                     part[kM * D + local] = m;
                     part[kM * D + kM + local] = l;
                 }
@@ -628,16 +708,16 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
             if (lane == 0) tc::mbar_arrive(o_free);
             if (c0 != c1) {
                 __threadfence();
-                tc::named_sync(5, kSoftWarps * 32);
+                tc::named_sync(13, kSoftWarps * 32);
                 if (tid == 0) {
                     const unsigned n = atomicAdd(p.counters + c0, 1u);
                     sm.last = n == (unsigned)(c1 - c0);
                     if (sm.last) p.counters[c0] = 0;  // as the next call finds it
                     __threadfence();
                 }
-                tc::named_sync(5, kSoftWarps * 32);
+                tc::named_sync(13, kSoftWarps * 32);
                 const bool join = sm.last != 0;
-                tc::named_sync(5, kSoftWarps * 32);
+                tc::named_sync(13, kSoftWarps * 32);
                 if (join) {
                     auto part_of = [&](int c) { return p.partials + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * kPart; };
                     m = -INFINITY;
@@ -652,14 +732,14 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = 0.0f;
                         for (int c = c0; c <= c1; ++c) {
-                            const float f = factor(__ldcg(part_of(c) + kM * D + local), m);
+                            const float fc = factor(__ldcg(part_of(c) + kM * D + local), m);
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
-                                const float4 v = __ldcg(reinterpret_cast<const float4*>(part_of(c)) + (half * (D / 8) + 8 * k + i) * kM + local);
-                                o[4 * i] = fmaf(v.x, f, o[4 * i]);
-                                o[4 * i + 1] = fmaf(v.y, f, o[4 * i + 1]);
-                                o[4 * i + 2] = fmaf(v.z, f, o[4 * i + 2]);
-                                o[4 * i + 3] = fmaf(v.w, f, o[4 * i + 3]);
+                                const float4 x = __ldcg(reinterpret_cast<const float4*>(part_of(c)) + (team * (D / 8) + 8 * k + i) * kM + local);
+                                o[4 * i] = fmaf(x.x, fc, o[4 * i]);
+                                o[4 * i + 1] = fmaf(x.y, fc, o[4 * i + 1]);
+                                o[4 * i + 2] = fmaf(x.z, fc, o[4 * i + 2]);
+                                o[4 * i + 3] = fmaf(x.w, fc, o[4 * i + 3]);
                             }
                         }
                         put(k, o, inv);
