@@ -9,11 +9,13 @@
 // over both, twice the products at twice bf16's rate, with half its bytes
 // of operands and no conversion of a tile.
 //
-// Roles of the CTA's sixteen warps: one loads tiles (TMA) and their scales; one
-// thread issues the MMAs; eight are the softmax, in two teams that take turns
-// at the tiles; six split the next item's q, fetched into the L2 an item ahead,
-// while the last tiles run.  The softmax warps hold 64 logits a thread: the
-// others give them registers (88 and 168 of the 128 that the launch has for each).
+// Roles of the CTA's 24 warps: one loads tiles (TMA) and their scales; one
+// issues the MMAs; sixteen are the softmax, in two teams that take turns at the
+// tiles, two threads a row; six split the next item's q, fetched into the L2 an
+// item ahead, while the last tiles run.  (A tile's softmax is a chain of
+// latencies -- logits out of tensor memory, maximum, exponentials at one every
+// 5.5 cycles of a lone pair of warps, stores -- so it is more warps that make it
+// short: eight of them took 3,400 cycles a tile and team.)
 // Tensor memory: two tiles of logits (2 x 128 columns), over which their
 // weights are written as the second product's A operand, and the output
 // (d columns).  Per tile j the tensor pipe runs S(j + 1), then O += P(j) V(j).
@@ -36,15 +38,16 @@
 namespace gdn {
 namespace {
 
-constexpr int kSoftWarps = 8, kQWarps = 6;
+constexpr int kSoftWarps = 16, kQWarps = 6;
 constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kQWarp0 = kSoftWarps + 2;
 constexpr int kThreads = (kSoftWarps + 2 + kQWarps) * 32;
+constexpr int kTeamWarps = kSoftWarps / 2;
 constexpr int kM = 128;                 // rows of an item
 constexpr int kN = 128;                 // tokens of a tile
 constexpr float kPExp = 5.0f;           // weights are held times 2^5
 constexpr float kGrow = 3.8f;           // 2^(5 + 3.8) = 446
 constexpr int kScaleRing = 8;
-constexpr int kSoftRegs = 168, kOtherRegs = 88;  // 256 x (168 + 88) = 512 x 128
+constexpr int kSoftRegs = 88, kOtherRegs = 64;  // 512 x 88 + 256 x 64 = 768 x 80
 constexpr int kMinTiles = 2;            // tiles a CTA takes at least
 constexpr uint64_t kDrainNs = 200000000ull;
 
@@ -54,11 +57,12 @@ struct TilesSmem {
     static constexpr int kSlots = D == 256 ? 4 : 8;
     alignas(1024) uint8_t q[2][kM * D];                       // hi, lo
     alignas(1024) uint8_t ring[kSlots][kSlot];
-    float4 scales[kScaleRing][2];                             // {key scale, log2 value scale} of 4 x 32 tokens
+    float4 scales[kScaleRing][4];                             // of 32 tokens: key scale, log2 of the value scale, 1 / value scale
     float rf[kM];
-    float ref[2][kM];                                         // the rows' references after each team's last tile
-    float ml[2][2][2][kM];                                    // by item: each team's reference and sum
-    alignas(16) uint8_t stage[kSoftWarps][32 * 64];           // a warp's 32 rows x 32 columns of output on their way out
+    float ref[2][2][kM];                                      // the rows' references after a team's tiles, two of them in turn
+    float top[2][2][kM];                                      // by team and half: the rows' maxima of a tile
+    float ml[2][2][kM], mr[2][2][2][kM];                      // by item: the teams' references; each half's sum
+    alignas(16) uint8_t stage[kSoftWarps][32 * 32];           // a warp's 32 rows x 16 columns of output on their way out
     alignas(8) uint64_t full[kSlots], empty[kSlots], s_full[2], p_ready[2], o_done[2], scales_full[kScaleRing];
     uint64_t q_full, q_empty, item_done, o_free, drained;
     long long scan[kThreads / 32];
@@ -236,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(s_full + 8 * i, 1);
             tc::mbar_init(o_done + 8 * i, 1);
-            tc::mbar_init(p_ready + 8 * i, kSoftWarps / 2);
+            tc::mbar_init(p_ready + 8 * i, kTeamWarps);
         }
         for (int i = 0; i < kScaleRing; ++i) tc::mbar_init(scales_full + 8 * i, 1);
         tc::mbar_init(q_full, kQWarps);
@@ -299,7 +303,6 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                     lv = lv_next;
                     lookup(j + 8);
                 }
-                float* sc = reinterpret_cast<float*>(sm.scales[g % kScaleRing]);
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv, ++u) {
                     const int slot = u % kSlots;
@@ -307,10 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                     if (kv == 0) {
                         // the place in the ring is free: its last readers were done before the
                         // weights of the tile whose keys lay in this slot were
-                        if ((lane >> 2) == k) {
-                            sc[2 * (lane & 3)] = ks;
-                            sc[2 * (lane & 3) + 1] = lv;
-                        }
+                        if ((lane >> 2) == k) sm.scales[g % kScaleRing][lane & 3] = make_float4(ks, lv, ex2(-lv), 0.0f);
                         __syncwarp();
                         if (lane == 0) tc::mbar_arrive(scales_full + 8 * (g % kScaleRing));
                     }
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int ks = 0; ks < kN / 32; ++ks)
-                        tc::mma_e4m3_ts(tO, a + part * 32 + ks * 8, v + (ks * 32 * 128 >> 4), id_o, part + ks > 0 || !pend_first);
+                        tc::mma_e4m3_ts(tO, a + (ks >> 1) * 64 + (ks & 1) * 8 + part * 16, v + (ks * 32 * 128 >> 4), id_o, part + ks > 0 || !pend_first);
                 tc::mma_commit(empty + 8 * slot);
                 tc::mma_commit(o_done + 8 * buf);
                 if (pend_last) tc::mma_commit(item_done);
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
         constexpr int kLanes = D / 16;              // of a row, 16 values each
         constexpr int kAtOnce = 32 / kLanes;        // rows of a warp's step
         const int sub = lane / kLanes, c = lane % kLanes;
-        constexpr int kBatch = 4;                   // steps whose loads go out together
+        constexpr int kBatch = 2;                   // steps whose loads go out together
         int item = 0;
         bool more = w.settle(p);
         for (; more; ++item) {
@@ -483,148 +483,150 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
     }
     } else {
         // ----------------------------------------------------------- softmax
-        // Team 0 has the even tiles of the CTA, team 1 the odd ones, a thread a
-        // row: one team's exponentials run while the other reads its logits.
+        // Team 0 has the even tiles of the CTA, team 1 the odd ones, a thread half a
+        // row: 64 tokens.  A half's weights replace the first 32 columns of its own
+        // logits (hi of its 64 tokens, then lo).
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-        const int quad = warp & 3, team = warp >> 2, local = quad * 32 + lane;
-        const uint32_t lanes = (uint32_t)(quad * 32) << 16, tS = tmem + lanes + team * 128;
+        const int quad = warp & 3, half = (warp >> 2) & 1, team = warp >> 3, local = quad * 32 + lane;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16, tS = tmem + lanes + team * 128 + half * 64;
+        // One barrier a tile, team and quad of lanes: both halves' maxima are there, and the
+        // other team's reference after the tile before (from its first half).
+        const int my_bar = 1 + 4 * team + quad, other_bar = 1 + 4 * (team ^ 1) + quad;
+        if (team == 1 && half == 0) tc::named_arrive(other_bar, 96);  // there is no tile before the first
         int g = 0, item = 0;
         for (; w.settle(p); w.advance(p), ++item) {
             const RowMap rows(p, w.t);
-            const int row = w.t * kM + local;
-            const bool have = row < w.r.n * p.G;
+            const bool have = w.t * kM + local < w.r.n * p.G;
             int qi, hg;
             rows.find(local, qi, hg);
             if (!have) qi = hg = 0;
             const int64_t at = (int64_t)(w.r.row0 + qi) * p.Hq + w.h * p.G + hg;
             const int base = w.r.L - w.r.n;
             const int seen = have ? base + qi + 1 : 0;
-            const unsigned long long tree = p.tree != nullptr && have ? (unsigned long long)p.tree[w.r.row0 + qi] : 0ull;
             const int all_see = max(0, min(w.r.L, p.tree != nullptr ? base : base + rows.q0 + 1));
             wait(q_full, item);
             const float rf = sm.rf[local];
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(q_empty);
-            float m = -INFINITY, l = 0.0f;  // l: this team's tiles', relative to m
+            float m = -INFINITY, l = 0.0f;  // l: this thread's, relative to m
             for (int j = w.j0; j < w.j1; ++j, ++g) {
                 if ((g & 1) != team) continue;
                 wait(scales_full + 8 * (g % kScaleRing), g / kScaleRing);
-                const float4 sc[2] = {sm.scales[g % kScaleRing][0], sm.scales[g % kScaleRing][1]};  // four stretches of 32 tokens
-                const float f[4] = {rf * sc[0].x, rf * sc[0].z, rf * sc[1].x, rf * sc[1].z};
-                const float v[4] = {sc[0].y, sc[0].w, sc[1].y, sc[1].w};
-                // the row's 128 tokens as bits: those below its limit, or below the tree and the nodes it sees
+                const float4 sc0 = sm.scales[g % kScaleRing][2 * half], sc1 = sm.scales[g % kScaleRing][2 * half + 1];
+                const float f0 = rf * sc0.x, f1 = rf * sc1.x;
+                // the thread's 64 tokens as bits: those below its limit, or below the tree and the nodes it sees
                 const bool masked = j * kN + kN > all_see;
-                uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+                uint32_t vis[2] = {~0u, ~0u};
                 if (masked) {
                     auto below = [](int n) { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1; };
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const int pos0 = j * kN + hf * 64, first = base - pos0;  // column of the tree's first node
-                        unsigned long long bits = below(seen - pos0);
-                        if (p.tree != nullptr) {
-                            bits = below(first) | (first >= 64 || first <= -64 ? 0ull : first >= 0 ? tree << first : tree >> -first);
-                            bits = have ? bits & below(w.r.L - pos0) : 0ull;
-                        }
-                        vis[2 * hf] = (uint32_t)bits;
-                        vis[2 * hf + 1] = (uint32_t)(bits >> 32);
+                    const int pos0 = j * kN + half * 64, first = base - pos0;  // column of the tree's first node
+                    unsigned long long bits = below(seen - pos0);
+                    if (p.tree != nullptr) {
+                        const unsigned long long tree = have ? (unsigned long long)p.tree[w.r.row0 + qi] : 0ull;
+                        bits = below(first) | (first >= 64 || first <= -64 ? 0ull : first >= 0 ? tree << first : tree >> -first);
+                        bits = have ? bits & below(w.r.L - pos0) : 0ull;
                     }
+                    vis[0] = (uint32_t)bits;
+                    vis[1] = (uint32_t)(bits >> 32);
                 }
                 wait(s_full + 8 * team, g >> 1);
                 tc::fence_after_sync();
 
-                // ---- the tile's maximum (the second half first: the first one's logits stay in registers)
-                float s[64], top = -INFINITY;
+                // ---- the tile's maximum
+                float top = -INFINITY;
 #pragma unroll 1
-                for (int hf = 1; hf >= 0; --hf) {
-                    tc::tmem_ld64(tS + hf * 64, s);
-                    const uint32_t vis0 = hf ? vis[2] : vis[0], vis1 = hf ? vis[3] : vis[1];
+                for (int c = 0; c < 2; ++c) {
+                    float s[32];
+                    tc::tmem_ld32(tS + c * 32, s);
                     if (masked) {
+                        const uint32_t bits = c ? vis[1] : vis[0];
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            s[k] = (vis0 >> k) & 1 ? s[k] : -INFINITY;
-                            s[k + 32] = (vis1 >> k) & 1 ? s[k + 32] : -INFINITY;
-                        }
+                        for (int k = 0; k < 32; ++k) s[k] = (bits >> k) & 1 ? s[k] : -INFINITY;
                     }
-                    float t8[8];
+                    float t4[4];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) t8[k] = fmaxf(fmaxf(s[8 * k], s[8 * k + 1]), s[8 * k + 2]);
+                    for (int k = 0; k < 4; ++k) t4[k] = fmaxf(fmaxf(s[8 * k], s[8 * k + 1]), s[8 * k + 2]);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) t8[k] = fmaxf(fmaxf(t8[k], s[8 * k + 3]), s[8 * k + 4]);
+                    for (int k = 0; k < 4; ++k) t4[k] = fmaxf(fmaxf(t4[k], s[8 * k + 3]), s[8 * k + 4]);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) t8[k] = fmaxf(fmaxf(t8[k], s[8 * k + 5]), fmaxf(s[8 * k + 6], s[8 * k + 7]));
-                    const float top0 = fmaxf(fmaxf(t8[0], t8[1]), fmaxf(t8[2], t8[3])), top1 = fmaxf(fmaxf(t8[4], t8[5]), fmaxf(t8[6], t8[7]));
-                    top = fmaxf(top, fmaxf(fmaf(top0, hf ? f[2] : f[0], hf ? v[2] : v[0]), fmaf(top1, hf ? f[3] : f[1], hf ? v[3] : v[1])));
+                    for (int k = 0; k < 4; ++k) t4[k] = fmaxf(fmaxf(t4[k], s[8 * k + 5]), fmaxf(s[8 * k + 6], s[8 * k + 7]));
+                    const float t = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                    top = fmaxf(top, fmaf(t, c ? f1 : f0, c ? sc1.y : sc0.y));
                 }
+                sm.top[team][half][local] = top;
+                tc::named_sync(my_bar, 96);
 
                 // ---- the reference: the other team's after the tile before, raised where this tile asks for it
-                if (g > 0) tc::named_sync(1 + 4 * team + quad, 64);
-                float ref = j > w.j0 ? sm.ref[team ^ 1][local] : -INFINITY;
+                top = fmaxf(top, sm.top[team][half ^ 1][local]);
+                float ref = j > w.j0 ? sm.ref[((g - 1) >> 1) & 1][team ^ 1][local] : -INFINITY;
                 const bool grows = ref > -INFINITY && top > ref + kGrow;
-                const float c = grows ? ex2(ref - top) : 1.0f;
+                const float old = ref;
                 if (ref == -INFINITY || grows) ref = fmaxf(ref, top);
-                sm.ref[team][local] = ref;
-                if (g + 1 < n_tiles) tc::named_arrive(1 + 4 * (team ^ 1) + quad, 64);
-                l *= factor(m, ref);
-                m = ref;
-                if (j > w.j0 && __any_sync(~0u, grows)) {
-                    // This tile's logits came after product g - 2, and product g waits for this team: the barrier
-                    // is in the phase of product g - 1 or just past it, which its parity tells apart.
-                    wait(o_done + 8 * (team ^ 1), (g - 1) >> 1);
-                    tc::fence_after_sync();
+                if (half == 0) {
+                    sm.ref[(g >> 1) & 1][team][local] = ref;  // (the second half of the other team may still read the last one)
+                    if (g + 1 < n_tiles) tc::named_arrive(other_bar, 96);
+                }
+                if (__any_sync(~0u, ref != m)) {
+                    l *= factor(m, ref);
+                    m = ref;
+                    if (j > w.j0 && __any_sync(~0u, grows)) {
+                        // This tile's logits came after product g - 2, and product g waits for this team: the barrier
+                        // is in the phase of product g - 1 or just past it, which its parity tells apart.
+                        wait(o_done + 8 * (team ^ 1), (g - 1) >> 1);
+                        tc::fence_after_sync();
+                        const float c = grows ? ex2(old - ref) : 1.0f;
 #pragma unroll 1
-                    for (int k = 0; k < D / 32; ++k) {
-                        float o[32];
-                        tc::tmem_ld32(tO + lanes + 32 * k, o);
+                        for (int k = 0; k < D / 64; ++k) {
+                            float o[32];
+                            tc::tmem_ld32(tO + lanes + half * (D / 2) + 32 * k, o);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] *= c;
-                        tc::tmem_st32(tO + lanes + 32 * k, o);
+                            for (int i = 0; i < 32; ++i) o[i] *= c;
+                            tc::tmem_st32(tO + lanes + half * (D / 2) + 32 * k, o);
+                        }
                     }
                 }
 
                 // ---- weights
                 const float shift = kPExp - (m == -INFINITY ? 0.0f : m);
 #pragma unroll 1
-                for (int hf = 0; hf < 2; ++hf) {
-                    if (hf) tc::tmem_ld64(tS + 64, s);
-                    const float f0 = hf ? f[2] : f[0], f1 = hf ? f[3] : f[1], v0 = hf ? v[2] : v[0], v1 = hf ? v[3] : v[1];
-                    const float a0 = v0 + shift, a1 = v1 + shift;
-                    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    uint32_t hi[16], lo[16];
+                for (int c = 0; c < 2; ++c) {
+                    float s[32];
+                    tc::tmem_ld32(tS + c * 32, s);
+                    const float f = c ? f1 : f0, a = (c ? sc1.y : sc0.y) + shift;
+                    float part[2] = {0.0f, 0.0f};
+                    uint32_t hi[8], lo[8];
                     if (!masked) {
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const float ff = k < 8 ? f0 : f1, a = k < 8 ? a0 : a1;
-                            const float e0 = ex2(fmaf(s[4 * k], ff, a)), e1 = ex2(fmaf(s[4 * k + 1], ff, a)),
-                                        e2 = ex2(fmaf(s[4 * k + 2], ff, a)), e3 = ex2(fmaf(s[4 * k + 3], ff, a));
-                            part[k < 8 ? 0 : 2] += e0 + e1;
-                            part[k < 8 ? 1 : 3] += e2 + e3;
+                        for (int k = 0; k < 8; ++k) {
+                            const float e0 = ex2(fmaf(s[4 * k], f, a)), e1 = ex2(fmaf(s[4 * k + 1], f, a)), e2 = ex2(fmaf(s[4 * k + 2], f, a)),
+                                        e3 = ex2(fmaf(s[4 * k + 3], f, a));
+                            part[0] += e0 + e1;
+                            part[1] += e2 + e3;
                             split4_f16(e0, e1, e2, e3, hi[k], lo[k]);
                         }
                     } else {
-                        const uint32_t vis0 = hf ? vis[2] : vis[0], vis1 = hf ? vis[3] : vis[1];
+                        const uint32_t bits = c ? vis[1] : vis[0];
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const float ff = k < 8 ? f0 : f1, a = k < 8 ? a0 : a1;
-                            const uint32_t bits = (k < 8 ? vis0 : vis1) >> (4 * (k & 7));
+                        for (int k = 0; k < 8; ++k) {
                             float e[4];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) e[i] = (bits >> i) & 1 ? ex2(fmaf(s[4 * k + i], ff, a)) : 0.0f;
-                            part[k < 8 ? 0 : 2] += e[0] + e[1];
-                            part[k < 8 ? 1 : 3] += e[2] + e[3];
+                            for (int i = 0; i < 4; ++i) e[i] = (bits >> (4 * k + i)) & 1 ? ex2(fmaf(s[4 * k + i], f, a)) : 0.0f;
+                            part[0] += e[0] + e[1];
+                            part[1] += e[2] + e[3];
                             split4_f16(e[0], e[1], e[2], e[3], hi[k], lo[k]);
                         }
                     }
-                    tc::tmem_st16(tS + hf * 16, hi);
-                    tc::tmem_st16(tS + 32 + hf * 16, lo);
+                    tc::tmem_st8(tS + c * 8, hi);
+                    tc::tmem_st8(tS + 16 + c * 8, lo);
                     // a row that sees nothing here takes nothing from the block's scale
-                    if (part[0] + part[1] != 0.0f) l = fmaf(part[0] + part[1], ex2(-v0), l);
-                    if (part[2] + part[3] != 0.0f) l = fmaf(part[2] + part[3], ex2(-v1), l);
+                    const float sum = part[0] + part[1];
+                    if (sum != 0.0f) l = fmaf(sum, c ? sc1.z : sc0.z, l);
                 }
                 if (j * kN + kN > w.r.L) {  // whatever lies past the end: zeros for the product
                     const int u = 2 * g + 1, slot = u % kSlots;
                     wait(full + 8 * slot, u / kSlots);
                     const int first = max(0, w.r.L - j * kN);
-                    for (int i = local; i < (kN - first) * (D / 16); i += kM) {
+                    for (int i = half * kM + local; i < (kN - first) * (D / 16); i += 2 * kM) {
                         const int tok = first + i / (D / 16), cc = i % (D / 16);
                         *reinterpret_cast<uint4*>(sm.ring[slot] + (cc >> 3) * kHalfBytes + tok * 128 + (cc & 7) * 16) = make_uint4(0, 0, 0, 0);
                     }
@@ -636,44 +638,49 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                 if (lane == 0) tc::mbar_arrive(p_ready + 8 * team);
             }
 
-            // ---- the item's output: whole, or this CTA's part of it.  Each team has half the columns.
-            sm.ml[item & 1][team][0][local] = m;
-            sm.ml[item & 1][team][1][local] = l;
-            tc::named_sync(9 + quad, 64);
+            // ---- the item's output: whole, or this CTA's part of it.  A team and half has a quarter of the columns.
+            const int part_id = team * 2 + half, col0 = part_id * (D / 4);
+            if (half == 0) sm.ml[item & 1][team][local] = m;
+            sm.mr[item & 1][team][half][local] = l;
+            tc::named_sync(9 + quad, 128);
             {
-                const float m0 = sm.ml[item & 1][0][0][local], m1 = sm.ml[item & 1][1][0][local];
+                const float m0 = sm.ml[item & 1][0][local], m1 = sm.ml[item & 1][1][local];
                 // the last tile's team has the final reference; O is relative to it
                 m = ((g - 1) & 1) == 0 ? m0 : m1;
-                l = sm.ml[item & 1][0][1][local] * factor(m0, m) + sm.ml[item & 1][1][1][local] * factor(m1, m);
+                l = (sm.mr[item & 1][0][0][local] + sm.mr[item & 1][0][1][local]) * factor(m0, m) +
+                    (sm.mr[item & 1][1][0][local] + sm.mr[item & 1][1][1][local]) * factor(m1, m);
             }
             const long long item0 = w.x - w.j0;
             const int c0 = (int)(item0 / W), c1 = (int)((item0 + w.kt - 1) / W);
-            // 32 columns from team * D / 2 + 32 k of the warp's 32 rows, through shared
-            // memory: a row's 64 bytes then leave from four lanes (a thread storing its own row
-            // would touch 32 lines with every instruction).
+            // 32 columns from col0 + 32 k of the warp's 32 rows, sixteen at a time through
+            // shared memory: a row's 32 bytes then leave from two lanes (a thread storing its
+            // own row would touch 32 lines with every instruction).
             const int rows_here = min(kM, w.r.n * p.G - w.t * kM);
             auto put = [&](int k, const float (&o)[32], float inv) {
                 uint4* stage = reinterpret_cast<uint4*>(sm.stage[warp]);
-                __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t u[4];
+                for (int h2 = 0; h2 < 2; ++h2) {
+                    __syncwarp();
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        u[e] = tc::pack_bf16(__float2bfloat16_rn(o[8 * i + 2 * e] * inv), __float2bfloat16_rn(o[8 * i + 2 * e + 1] * inv));
-                    stage[lane * 4 + (i ^ ((lane >> 1) & 3))] = make_uint4(u[0], u[1], u[2], u[3]);
-                }
-                __syncwarp();
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t u[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = i * 8 + (lane >> 2);
-                    const int64_t to = __shfl_sync(~0u, at, r);
-                    if (quad * 32 + r < rows_here)
-                        reinterpret_cast<uint4*>(p.out + to * D + team * (D / 2) + 32 * k)[lane & 3] = stage[r * 4 + ((lane & 3) ^ ((r >> 1) & 3))];
+                        for (int e = 0; e < 4; ++e)
+                            u[e] = tc::pack_bf16(__float2bfloat16_rn(o[16 * h2 + 8 * i + 2 * e] * inv), __float2bfloat16_rn(o[16 * h2 + 8 * i + 2 * e + 1] * inv));
+                        stage[lane * 2 + (i ^ ((lane >> 2) & 1))] = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = i * 16 + (lane >> 1);
+                        const int64_t to = __shfl_sync(~0u, at, r);
+                        if (quad * 32 + r < rows_here)
+                            reinterpret_cast<uint4*>(p.out + to * D + col0 + 32 * k + 16 * h2)[lane & 1] = stage[r * 2 + ((lane & 1) ^ ((r >> 2) & 1))];
+                    }
                 }
             };
             auto put_lse = [&]() {
-                if (p.lse != nullptr && have && team == 0)
+                if (p.lse != nullptr && have && part_id == 0)
                     p.lse[at] = l == 0.0f ? -INFINITY : ((m == -INFINITY ? 0.0f : m) - kPExp + log2f(l)) * 0.69314718055994531f;
             };
             wait(item_done, item);
@@ -681,24 +688,24 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
             if (c0 == c1) {
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no token seen: zeros
 #pragma unroll 1
-                for (int k = 0; k < D / 64; ++k) {
+                for (int k = 0; k < D / 128; ++k) {
                     float o[32];
-                    tc::tmem_ld32(tO + lanes + team * (D / 2) + 32 * k, o);
+                    tc::tmem_ld32(tO + lanes + col0 + 32 * k, o);
                     put(k, o, inv);
                 }
                 put_lse();
             } else {
                 float* part = p.partials + ((size_t)blockIdx.x * 2 + (w.j0 == 0 ? 1 : 0)) * kPart;
 #pragma unroll 1
-                for (int k = 0; k < D / 64; ++k) {
+                for (int k = 0; k < D / 128; ++k) {
                     float o[32];
-                    tc::tmem_ld32(tO + lanes + team * (D / 2) + 32 * k, o);
+                    tc::tmem_ld32(tO + lanes + col0 + 32 * k, o);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        reinterpret_cast<float4*>(part)[(team * (D / 8) + 8 * k + i) * kM + local] =
+                        reinterpret_cast<float4*>(part)[(col0 / 4 + 8 * k + i) * kM + local] =
                             make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                 }
-                if (team == 0) {
+                if (part_id == 0) {
                     part[kM * D + local] = m;
                     part[kM * D + kM + local] = l;
                 }
@@ -727,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                         l = fmaf(__ldcg(part_of(c) + kM * D + kM + local), factor(__ldcg(part_of(c) + kM * D + local), m), l);
                     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
-                    for (int k = 0; k < D / 64; ++k) {
+                    for (int k = 0; k < D / 128; ++k) {
                         float o[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = 0.0f;
@@ -735,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                             const float fc = factor(__ldcg(part_of(c) + kM * D + local), m);
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
-                                const float4 x = __ldcg(reinterpret_cast<const float4*>(part_of(c)) + (team * (D / 8) + 8 * k + i) * kM + local);
+                                const float4 x = __ldcg(reinterpret_cast<const float4*>(part_of(c)) + (col0 / 4 + 8 * k + i) * kM + local);
                                 o[4 * i] = fmaf(x.x, fc, o[4 * i]);
                                 o[4 * i + 1] = fmaf(x.y, fc, o[4 * i + 1]);
                                 o[4 * i + 2] = fmaf(x.z, fc, o[4 * i + 2]);
