@@ -16,9 +16,10 @@
 // latencies -- logits out of tensor memory, maximum, exponentials at one every
 // 5.5 cycles of a lone pair of warps, stores -- so it is more warps that make it
 // short: eight of them took 3,400 cycles a tile and team.)
-// Tensor memory: two tiles of logits (2 x 128 columns), over which their
-// weights are written as the second product's A operand, and the output
-// (d columns).  Per tile j the tensor pipe runs S(j + 1), then O += P(j) V(j).
+// Tensor memory: tiles of logits (128 columns each: two for d = 256, three for
+// 128), over which their weights are written as the second product's A operand,
+// and the output (d columns).  The tensor pipe runs the logits of one or two
+// tiles ahead, then O += P V of the tile whose weights are ready.
 //
 // The reference m of a row is raised, and the output rescaled in tensor
 // memory, only when a tile's maximum exceeds it by more than 2^3.8: weights
@@ -48,26 +49,29 @@ constexpr float kPExp = 5.0f;           // weights are held times 2^5
 constexpr float kGrow = 3.8f;           // 2^(5 + 3.8) = 446
 constexpr int kScaleRing = 8;
 constexpr int kSoftRegs = 88, kOtherRegs = 64;  // 512 x 88 + 256 x 64 = 768 x 80
-constexpr int kMinTiles = 2;            // tiles a CTA takes at least
+constexpr int kItemCost = 4;            // an item's beginning and end, in tiles
+constexpr int kMinTiles = 8;            // what a CTA takes at least
 constexpr uint64_t kDrainNs = 200000000ull;
 
 template <int D>
 struct TilesSmem {
     static constexpr int kSlot = kN * D;                      // a tile's keys or values
     static constexpr int kSlots = D == 256 ? 4 : 8;
-    alignas(1024) uint8_t q[2][kM * D];                       // hi, lo
+    static constexpr int kBufs = D == 256 ? 2 : 3;            // tiles of logits in tensor memory
+    static constexpr int kQBufs = D == 256 ? 1 : 2;           // items' q
+    alignas(1024) uint8_t q[kQBufs][2][kM * D];               // hi, lo
     alignas(1024) uint8_t ring[kSlots][kSlot];
     float4 scales[kScaleRing][4];                             // of 32 tokens: key scale, log2 of the value scale, 1 / value scale
-    float rf[kM];
+    float rf[kQBufs][kM];
     float ref[2][2][kM];                                      // the rows' references after a team's tiles, two of them in turn
-    float top[2][2][kM];                                      // by team and half: the rows' maxima of a tile
+    float top[2][2][2][kM];                                   // by team and half: the rows' maxima of two tiles in turn
     float ml[2][2][kM], mr[2][2][2][kM];                      // by item: the teams' references; each half's sum
     alignas(16) uint8_t stage[kSoftWarps][32 * 32];           // a warp's 32 rows x 16 columns of output on their way out
-    alignas(8) uint64_t full[kSlots], empty[kSlots], s_full[2], p_ready[2], o_done[2], scales_full[kScaleRing];
-    uint64_t q_full, q_empty, item_done, o_free, drained;
+    alignas(8) uint64_t full[kSlots], empty[kSlots], s_full[kBufs], p_ready[kBufs], o_done[2], scales_full[kScaleRing];
+    uint64_t q_full[kQBufs], q_empty[kQBufs], item_done, o_free, drained;
     long long scan[kThreads / 32];
     int qbase[kThreads];
-    int at_b, at_t, at_h, at_j;
+    int at_b, at_t, at_h, at_v;
     unsigned last;
     uint32_t tmem;
     int dead;
@@ -94,31 +98,38 @@ __device__ __forceinline__ int token_tiles(const KvAttnParams& p, const Request&
     return max(1, (seen + kN - 1) / kN);
 }
 
-// One stretch of an item's token tiles, and the walk over a CTA's stretches.
+// One stretch of an item's token tiles, and the walk over a CTA's stretches.  An
+// item takes kItemCost places of the list before its tiles' own, so that CTAs
+// with many short items get fewer tiles.
 struct Walk {
-    int b, t, h, j0, j1, kt;
+    int b, t, h, v0, j0, j1, kt;
     long long x, x1;
     Request r;
     __device__ __forceinline__ bool settle(const KvAttnParams& p) {  // false: the CTA's part is done
-        if (x >= x1) return false;
-        r = request(p, b);
-        while (t >= r.tiles) {
-            t = 0;
-            ++b;
+        while (x < x1) {
             r = request(p, b);
+            while (t >= r.tiles) {
+                t = 0;
+                r = request(p, ++b);
+            }
+            kt = token_tiles(p, r, t);
+            const int v1 = (int)min((long long)kt + kItemCost, v0 + (x1 - x));
+            j0 = max(0, v0 - kItemCost);
+            j1 = max(0, v1 - kItemCost);
+            if (j0 < j1) return true;
+            next(p, v1);
         }
-        kt = token_tiles(p, r, t);
-        j1 = (int)min((long long)kt, j0 + (x1 - x));
-        return true;
+        return false;
     }
-    __device__ __forceinline__ void advance(const KvAttnParams& p) {
-        x += j1 - j0;
-        j0 = 0;
-        if (j1 == kt && ++h == p.Hkv) {
+    __device__ __forceinline__ void next(const KvAttnParams& p, int v1) {
+        x += v1 - v0;
+        v0 = 0;
+        if (++h == p.Hkv) {
             h = 0;
             ++t;
         }
     }
+    __device__ __forceinline__ void advance(const KvAttnParams& p) { next(p, j1 + kItemCost); }
 };
 
 // Rows of an item -> query and head of the group, without a division for each:
@@ -144,7 +155,7 @@ __device__ __forceinline__ float factor(float m, float top) { return m == top ? 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __grid_constant__ KvAttnParams p) {
     using Smem = TilesSmem<D>;
-    constexpr int kSlot = Smem::kSlot, kSlots = Smem::kSlots, kHalves = D / 128;
+    constexpr int kSlot = Smem::kSlot, kSlots = Smem::kSlots, kBufs = Smem::kBufs, kQBufs = Smem::kQBufs, kHalves = D / 128;
     constexpr uint32_t kHalfBytes = kN * 128;
     constexpr int kPart = kM * D + 2 * kM;
     extern __shared__ uint8_t smem_raw[];
@@ -196,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                 t = 0;
                 r = request(p, ++b);
             }
-            mine += token_tiles(p, r, t);
+            mine += token_tiles(p, r, t) + kItemCost;
         }
     }
     const long long before = scan(mine, total) * p.Hkv;
@@ -213,22 +224,22 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                 t = 0;
                 r = request(p, ++b);
             }
-            const int kt = token_tiles(p, r, t);
-            if (rest < (long long)kt * p.Hkv) {
+            const int len = token_tiles(p, r, t) + kItemCost;
+            if (rest < (long long)len * p.Hkv) {
                 sm.at_b = b;
                 sm.at_t = t;
-                sm.at_h = (int)(rest / kt);
-                sm.at_j = (int)(rest % kt);
+                sm.at_h = (int)(rest / len);
+                sm.at_v = (int)(rest % len);
                 break;
             }
-            rest -= (long long)kt * p.Hkv;
+            rest -= (long long)len * p.Hkv;
         }
     }
 
     // ---- barriers and tensor memory
     const uint32_t full = tc::smem_u32(sm.full), empty = tc::smem_u32(sm.empty), s_full = tc::smem_u32(sm.s_full),
                    p_ready = tc::smem_u32(sm.p_ready), scales_full = tc::smem_u32(sm.scales_full),
-                   q_full = tc::smem_u32(&sm.q_full), q_empty = tc::smem_u32(&sm.q_empty),
+                   q_full = tc::smem_u32(sm.q_full), q_empty = tc::smem_u32(sm.q_empty),
                    o_done = tc::smem_u32(sm.o_done), o_free = tc::smem_u32(&sm.o_free), item_done = tc::smem_u32(&sm.item_done),
                    drained = tc::smem_u32(&sm.drained);
     if (tid == 0) {
@@ -237,14 +248,16 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
             tc::mbar_init(full + 8 * i, 1);
             tc::mbar_init(empty + 8 * i, 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kBufs; ++i) {
             tc::mbar_init(s_full + 8 * i, 1);
-            tc::mbar_init(o_done + 8 * i, 1);
             tc::mbar_init(p_ready + 8 * i, kTeamWarps);
         }
         for (int i = 0; i < kScaleRing; ++i) tc::mbar_init(scales_full + 8 * i, 1);
-        tc::mbar_init(q_full, kQWarps);
-        tc::mbar_init(q_empty, 1 + kSoftWarps);
+        for (int i = 0; i < kQBufs; ++i) {
+            tc::mbar_init(q_full + 8 * i, kQWarps);
+            tc::mbar_init(q_empty + 8 * i, 1 + kSoftWarps);
+        }
+        for (int i = 0; i < 2; ++i) tc::mbar_init(o_done + 8 * i, 1);
         tc::mbar_init(o_free, kSoftWarps);
         tc::mbar_init(item_done, 1);
         tc::mbar_init(drained, 1);
@@ -253,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = sm.tmem, tO = tmem + 256;  // logits and weights in columns 0 .. 255
+    const uint32_t tmem = sm.tmem, tO = tmem + kBufs * kN;  // logits and weights before the output
     volatile int* dead = &sm.dead;
 
     // A bounded wait.  The first that gives up ends all waiting (and all
@@ -266,12 +279,11 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
         }
     };
 
-    const int n_tiles = (int)(x1 - x0);
     Walk w;
     w.b = sm.at_b;
     w.t = sm.at_t;
     w.h = sm.at_h;
-    w.j0 = sm.at_j;
+    w.v0 = sm.at_v;
     w.x = x0;
     w.x1 = x1;
 
@@ -338,45 +350,50 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
         // its descriptors from uniform registers: under a test of the lane number
         // instead, each one costs about 185 cycles of issue, three times its own 64.)
         constexpr uint32_t id_s = tc::idesc_e4m3(kM, kN, false), id_o = tc::idesc_e4m3(kM, D, true);
-        const uint64_t q_hi = tc::smem_desc_sw128(tc::smem_u32(sm.q[0])), q_lo = tc::smem_desc_sw128(tc::smem_u32(sm.q[1]));
         const uint32_t ring = tc::smem_u32(sm.ring[0]);
-        int g = 0, item = 0;
-        bool pending = false, pend_first = false, pend_last = false;  // the weights' product of tile g - 1
-        int pend_item = 0;
+        int gs = 0, gp = 0;                       // tiles whose logits, whose product have been issued
+        uint32_t firsts = 0, lasts = 0;           // of the items, by tile modulo 32
+        int item = 0, item_p = 0;
         auto product = [&]() {
-            if (!pending) return;
-            pending = false;
-            const int gp = g - 1, u = 2 * gp + 1, slot = u % kSlots, buf = gp & 1;
-            if (pend_first && pend_item > 0) wait(o_free, pend_item - 1);
+            const int u = 2 * gp + 1, slot = u % kSlots, buf = gp % kBufs;
+            const bool first = (firsts >> (gp & 31)) & 1, last = (lasts >> (gp & 31)) & 1;
+            if (first && item_p > 0) wait(o_free, item_p - 1);
             wait(full + 8 * slot, u / kSlots);
-            wait(p_ready + 8 * buf, gp >> 1);
-            if (*dead) return;
-            tc::fence_after_sync();
-            const uint64_t v = tc::smem_desc_mn_sw128(ring + slot * kSlot, kHalfBytes);
-            const uint32_t a = tmem + buf * 128;
-            if (tc::elect_one()) {
+            wait(p_ready + 8 * buf, gp / kBufs);
+            if (!*dead) {
+                tc::fence_after_sync();
+                const uint64_t v = tc::smem_desc_mn_sw128(ring + slot * kSlot, kHalfBytes);
+                const uint32_t a = tmem + buf * kN;
+                if (tc::elect_one()) {
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
+                    for (int part = 0; part < 2; ++part)
 #pragma unroll
-                    for (int ks = 0; ks < kN / 32; ++ks)
-                        tc::mma_e4m3_ts(tO, a + (ks >> 1) * 64 + (ks & 1) * 8 + part * 16, v + (ks * 32 * 128 >> 4), id_o, part + ks > 0 || !pend_first);
-                tc::mma_commit(empty + 8 * slot);
-                tc::mma_commit(o_done + 8 * buf);
-                if (pend_last) tc::mma_commit(item_done);
+                        for (int ks = 0; ks < kN / 32; ++ks)
+                            tc::mma_e4m3_ts(tO, a + (ks >> 1) * 64 + (ks & 1) * 8 + part * 16, v + (ks * 32 * 128 >> 4), id_o, part + ks > 0 || !first);
+                    tc::mma_commit(empty + 8 * slot);
+                    tc::mma_commit(o_done + 8 * (gp & 1));
+                    if (last) tc::mma_commit(item_done);
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            if (last) ++item_p;
+            ++gp;
         };
         for (; w.settle(p); w.advance(p), ++item) {
-            // the last item's product first, unless this item's q is there already
-            if (!__all_sync(~0u, tc::mbar_test(q_full, item & 1))) product();
-            wait(q_full, item);
+            const int qb = item % kQBufs;
+            // the products that are due first, unless this item's q is there already
+            if (!__all_sync(~0u, tc::mbar_test(q_full + 8 * qb, (item / kQBufs) & 1)))
+                while (gp < gs) product();
+            wait(q_full + 8 * qb, item / kQBufs);
+            const uint64_t q_hi = tc::smem_desc_sw128(tc::smem_u32(sm.q[0][0]) + qb * 2 * kM * D), q_lo = q_hi + (kM * D >> 4);
             for (int j = w.j0; j < w.j1; ++j) {
-                const int u = 2 * g, slot = u % kSlots, buf = g & 1;
+                while (gp <= gs - kBufs) product();  // the buffer's last reader
+                const int u = 2 * gs, slot = u % kSlots, buf = gs % kBufs;
                 wait(full + 8 * slot, u / kSlots);
                 if (!*dead) {
                     tc::fence_after_sync();
                     const uint64_t k = tc::smem_desc_sw128(ring + slot * kSlot);
-                    const uint32_t d = tmem + buf * 128;
+                    const uint32_t d = tmem + buf * kN;
                     if (tc::elect_one()) {
 #pragma unroll
                         for (int part = 0; part < 2; ++part)
@@ -387,19 +404,17 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                             }
                         tc::mma_commit(empty + 8 * slot);
                         tc::mma_commit(s_full + 8 * buf);
-                        if (j == w.j1 - 1) tc::mma_commit(q_empty);
+                        if (j == w.j1 - 1) tc::mma_commit(q_empty + 8 * qb);
                     }
                     __syncwarp();
                 }
-                product();
-                ++g;
-                pending = true;
-                pend_first = j == w.j0;
-                pend_last = j == w.j1 - 1;
-                pend_item = item;
+                const uint32_t bit = 1u << (gs & 31);
+                firsts = j == w.j0 ? firsts | bit : firsts & ~bit;
+                lasts = j == w.j1 - 1 ? lasts | bit : lasts & ~bit;
+                ++gs;
             }
         }
-        product();
+        while (gp < gs) product();
         // every MMA has ended before tensor memory is given back
         if (tc::elect_one()) tc::mma_commit(drained);
         __syncwarp();
@@ -411,11 +426,26 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
         const int sub = lane / kLanes, c = lane % kLanes;
         constexpr int kBatch = 2;                   // steps whose loads go out together
         int item = 0;
+        auto fetch = [&]() {  // an item's rows towards the L2 (a row is 2 or 4 lines)
+            const int rows_next = w.r.n * p.G - w.t * kM;
+            const RowMap map_next(p, w.t);
+#pragma unroll 1
+            for (int i = (warp - kQWarp0) * 32 + lane; i < kM * (D / 64); i += kQWarps * 32) {
+                const int local = i / (D / 64);
+                if (local < rows_next) {
+                    int qi, hg;
+                    map_next.find(local, qi, hg);
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + (int64_t)(w.r.row0 + qi) * p.ldq + (int64_t)(w.h * p.G + hg) * D + (i % (D / 64)) * 64));
+                }
+            }
+        };
         bool more = w.settle(p);
+        if (more) fetch();
         for (; more; ++item) {
             const int rows = w.r.n * p.G - w.t * kM;  // of this item
             const RowMap map(p, w.t);
-            bool waited = item == 0;
+            const int qb = item % kQBufs;
+            bool waited = item < kQBufs;
 #pragma unroll 1
             for (int i0 = warp - kQWarp0; i0 < kM / kAtOnce; i0 += kBatch * kQWarps) {
                 uint4 x[kBatch][2];
@@ -431,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                         x[i][1] = src[1];
                     }
                 }
-                if (!waited) wait(q_empty, item - 1);
+                if (!waited) wait(q_empty + 8 * qb, item / kQBufs - 1);
                 waited = true;
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
@@ -455,30 +485,18 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                                    __uint_as_float(b & 0xffff0000u) * inv, hi[k], lo[k]);
                     }
                     const uint32_t at = (c >> 3) * (kM * 128) + local * 128 + (((c & 7) ^ (local & 7)) << 4);
-                    *reinterpret_cast<uint4*>(sm.q[0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(sm.q[1] + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    *reinterpret_cast<uint4*>(sm.q[qb][0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(sm.q[qb][1] + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     // a query that is not finite makes its row NaN, through the row's factor
-                    if (c == 0) sm.rf[local] = finite ? exp2_int(e) * p.scale_log2 : __int_as_float(0x7fffffff);
+                    if (c == 0) sm.rf[qb][local] = finite ? exp2_int(e) * p.scale_log2 : __int_as_float(0x7fffffff);
                 }
             }
             tc::fence_async_smem();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(q_full);
+            if (lane == 0) tc::mbar_arrive(q_full + 8 * qb);
             w.advance(p);
             more = w.settle(p);
-            if (more) {  // the next item's rows towards the L2 (a row is 2 or 4 lines)
-                const int rows_next = w.r.n * p.G - w.t * kM;
-                const RowMap map_next(p, w.t);
-#pragma unroll 1
-                for (int i = (warp - kQWarp0) * 32 + lane; i < kM * (D / 64); i += kQWarps * 32) {
-                    const int local = i / (D / 64);
-                    if (local < rows_next) {
-                        int qi, hg;
-                        map_next.find(local, qi, hg);
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + (int64_t)(w.r.row0 + qi) * p.ldq + (int64_t)(w.h * p.G + hg) * D + (i % (D / 64)) * 64));
-                    }
-                }
-            }
+            if (more) fetch();
         }
     }
     } else {
@@ -488,13 +506,18 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
         // logits (hi of its 64 tokens, then lo).
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         const int quad = warp & 3, half = (warp >> 2) & 1, team = warp >> 3, local = quad * 32 + lane;
-        const uint32_t lanes = (uint32_t)(quad * 32) << 16, tS = tmem + lanes + team * 128 + half * 64;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16, tH = tmem + lanes + half * 64;
         // One barrier a tile, team and quad of lanes: both halves' maxima are there, and the
         // other team's reference after the tile before (from its first half).
         const int my_bar = 1 + 4 * team + quad, other_bar = 1 + 4 * (team ^ 1) + quad;
-        if (team == 1 && half == 0) tc::named_arrive(other_bar, 96);  // there is no tile before the first
         int g = 0, item = 0;
-        for (; w.settle(p); w.advance(p), ++item) {
+        Walk w_next = w;
+        bool more = w_next.settle(p);
+        if (more && team == 1 && half == 0) tc::named_arrive(other_bar, 96);  // there is no tile before the first
+        for (; more; ++item) {
+            w = w_next;
+            w_next.advance(p);
+            more = w_next.settle(p);
             const RowMap rows(p, w.t);
             const bool have = w.t * kM + local < w.r.n * p.G;
             int qi, hg;
@@ -504,13 +527,16 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
             const int base = w.r.L - w.r.n;
             const int seen = have ? base + qi + 1 : 0;
             const int all_see = max(0, min(w.r.L, p.tree != nullptr ? base : base + rows.q0 + 1));
-            wait(q_full, item);
-            const float rf = sm.rf[local];
+            const int qb = item % kQBufs;
+            wait(q_full + 8 * qb, item / kQBufs);
+            const float rf = sm.rf[qb][local];
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(q_empty);
+            if (lane == 0) tc::mbar_arrive(q_empty + 8 * qb);
             float m = -INFINITY, l = 0.0f;  // l: this thread's, relative to m
             for (int j = w.j0; j < w.j1; ++j, ++g) {
                 if ((g & 1) != team) continue;
+                const int buf = g % kBufs;
+                const uint32_t tS = tH + buf * kN;
                 wait(scales_full + 8 * (g % kScaleRing), g / kScaleRing);
                 const float4 sc0 = sm.scales[g % kScaleRing][2 * half], sc1 = sm.scales[g % kScaleRing][2 * half + 1];
                 const float f0 = rf * sc0.x, f1 = rf * sc1.x;
@@ -529,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                     vis[0] = (uint32_t)bits;
                     vis[1] = (uint32_t)(bits >> 32);
                 }
-                wait(s_full + 8 * team, g >> 1);
+                wait(s_full + 8 * buf, g / kBufs);
                 tc::fence_after_sync();
 
                 // ---- the tile's maximum
@@ -553,18 +579,18 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                     const float t = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                     top = fmaxf(top, fmaf(t, c ? f1 : f0, c ? sc1.y : sc0.y));
                 }
-                sm.top[team][half][local] = top;
+                sm.top[(g >> 1) & 1][team][half][local] = top;
                 tc::named_sync(my_bar, 96);
 
                 // ---- the reference: the other team's after the tile before, raised where this tile asks for it
-                top = fmaxf(top, sm.top[team][half ^ 1][local]);
+                top = fmaxf(top, sm.top[(g >> 1) & 1][team][half ^ 1][local]);
                 float ref = j > w.j0 ? sm.ref[((g - 1) >> 1) & 1][team ^ 1][local] : -INFINITY;
                 const bool grows = ref > -INFINITY && top > ref + kGrow;
                 const float old = ref;
                 if (ref == -INFINITY || grows) ref = fmaxf(ref, top);
                 if (half == 0) {
                     sm.ref[(g >> 1) & 1][team][local] = ref;  // (the second half of the other team may still read the last one)
-                    if (g + 1 < n_tiles) tc::named_arrive(other_bar, 96);
+                    if (j + 1 < w.j1 || more) tc::named_arrive(other_bar, 96);
                 }
                 if (__any_sync(~0u, ref != m)) {
                     l *= factor(m, ref);
@@ -635,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(p_ready + 8 * team);
+                if (lane == 0) tc::mbar_arrive(p_ready + 8 * buf);
             }
 
             // ---- the item's output: whole, or this CTA's part of it.  A team and half has a quarter of the columns.
@@ -650,8 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                 l = (sm.mr[item & 1][0][0][local] + sm.mr[item & 1][0][1][local]) * factor(m0, m) +
                     (sm.mr[item & 1][1][0][local] + sm.mr[item & 1][1][1][local]) * factor(m1, m);
             }
-            const long long item0 = w.x - w.j0;
-            const int c0 = (int)(item0 / W), c1 = (int)((item0 + w.kt - 1) / W);
+            const long long tile0 = w.x - w.v0 + kItemCost;  // the place of the item's first tile
+            const int c0 = (int)(tile0 / W), c1 = (int)((tile0 + w.kt - 1) / W);
             // 32 columns from col0 + 32 k of the warp's 32 rows, sixteen at a time through
             // shared memory: a row's 32 bytes then leave from two lanes (a thread storing its
             // own row would touch 32 lines with every instruction).
