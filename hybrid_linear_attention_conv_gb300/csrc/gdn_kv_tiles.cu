@@ -269,11 +269,14 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
     const uint32_t tmem = sm.tmem, tO = tmem + kBufs * kN;  // logits and weights before the output
     volatile int* dead = &sm.dead;
 
-    // A bounded wait.  The first that gives up ends all waiting (and all
-    // copies and MMAs) of the CTA: the roles run through, the status word tells.
+    // A bounded wait.  The first that gives up ends all waiting of the CTA, and its
+    // copies: the roles run through on whatever is there, and the status word tells.
+    // (Arrivals without bytes may then come in any number: a phase just completes.)
     auto wait = [&](uint32_t bar, uint32_t parity) {
+        parity &= 1;
+        if (tc::mbar_test(bar, parity)) return;
         if (*dead) return;
-        if (!tc::mbar_wait(bar, parity & 1, p.wait_ns)) {
+        if (!tc::mbar_wait(bar, parity, p.wait_ns)) {
             *dead = 1;
             atomicOr(p.status, 2);
         }
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ tiles
         const int page_rows = min(1 << p.log2_page, kN), boxes = kN / page_rows;
-        int u = 0, g = 0;  // ring units (keys, values), tiles
+        int u = 0, g = 0, issued = 0;  // ring units (keys, values), tiles
         for (; w.settle(p); w.advance(p)) {
             // eight tiles' places and scales at a time: lane = 4 tile + 32-token stretch
             int y = 0, y_next = 0;
@@ -326,7 +329,10 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                         __syncwarp();
                         if (lane == 0) tc::mbar_arrive(scales_full + 8 * (g % kScaleRing));
                     }
+                    // Never into a slot whose wait gave up: a second arrival in a phase that still
+                    // awaits its bytes is a fault.  (A wait that returned for `dead` sees it set here.)
                     if (*dead) continue;
+                    issued = u + 1;
                     const uint32_t dst = tc::smem_u32(sm.ring[slot]);
                     if (lane == 0) tc::mbar_arrive_expect_tx(full + 8 * slot, kSlot);
                     for (int i = 0; i < boxes; ++i) {
@@ -341,9 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
             }
         }
         // Copies that nobody waited for (after a wait that gave up) land before the CTA ends.
-        if (*dead && lane == 0)
-            for (int i = 0; i < kSlots; ++i)
-                for (uint32_t par = 0; par < 2; ++par) tc::mbar_wait(full + 8 * i, par, kDrainNs / 20);
+        for (int i = max(0, issued - kSlots); i < issued; ++i) tc::mbar_wait(full + 8 * (i % kSlots), (i / kSlots) & 1, kDrainNs);
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------- MMAs
         // The whole warp walks and waits; one elected lane issues.  (An MMA takes
@@ -360,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
             if (first && item_p > 0) wait(o_free, item_p - 1);
             wait(full + 8 * slot, u / kSlots);
             wait(p_ready + 8 * buf, gp / kBufs);
-            if (!*dead) {
+            {
                 tc::fence_after_sync();
                 const uint64_t v = tc::smem_desc_mn_sw128(ring + slot * kSlot, kHalfBytes);
                 const uint32_t a = tmem + buf * kN;
@@ -390,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                 while (gp <= gs - kBufs) product();  // the buffer's last reader
                 const int u = 2 * gs, slot = u % kSlots, buf = gs % kBufs;
                 wait(full + 8 * slot, u / kSlots);
-                if (!*dead) {
+                {
                     tc::fence_after_sync();
                     const uint64_t k = tc::smem_desc_sw128(ring + slot * kSlot);
                     const uint32_t d = tmem + buf * kN;
