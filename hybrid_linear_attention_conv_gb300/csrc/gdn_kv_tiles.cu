@@ -40,7 +40,7 @@ namespace gdn {
 namespace {
 
 constexpr int kSoftWarps = 16, kQWarps = 6;
-constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kQWarp0 = kSoftWarps + 2;
+constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kQWarp0 = kSoftWarps + 2, kMmaWarp2 = kSoftWarps + 7;
 constexpr int kThreads = (kSoftWarps + 2 + kQWarps) * 32;
 constexpr int kTeamWarps = kSoftWarps / 2;
 constexpr int kM = 128;                 // rows of an item
@@ -59,6 +59,7 @@ struct TilesSmem {
     static constexpr int kSlots = D == 256 ? 4 : 8;
     static constexpr int kBufs = D == 256 ? 2 : 3;            // tiles of logits in tensor memory
     static constexpr int kQBufs = D == 256 ? 1 : 2;           // items' q
+    static constexpr bool kTwo = D == 128;                    // two warps issue MMAs
     alignas(1024) uint8_t q[kQBufs][2][kM * D];               // hi, lo
     alignas(1024) uint8_t ring[kSlots][kSlot];
     float4 scales[kScaleRing][4];                             // of 32 tokens: key scale, log2 of the value scale, 1 / value scale
@@ -67,7 +68,7 @@ struct TilesSmem {
     float top[2][2][2][kM];                                   // by team and half: the rows' maxima of two tiles in turn
     float ml[2][2][kM], mr[2][2][2][kM];                      // by item: the teams' references; each half's sum
     alignas(16) uint8_t stage[kSoftWarps][32 * 32];           // a warp's 32 rows x 16 columns of output on their way out
-    alignas(8) uint64_t full[kSlots], empty[kSlots], s_full[kBufs], p_ready[kBufs], o_done[2], scales_full[kScaleRing];
+    alignas(8) uint64_t full[kSlots], empty[kSlots], s_full[kBufs], p_ready[kBufs], o_done[kBufs], scales_full[kScaleRing];
     uint64_t q_full[kQBufs], q_empty[kQBufs], item_done, o_free, drained;
     long long scan[kThreads / 32];
     int qbase[kThreads];
@@ -156,6 +157,8 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __grid_constant__ KvAttnParams p) {
     using Smem = TilesSmem<D>;
     constexpr int kSlot = Smem::kSlot, kSlots = Smem::kSlots, kBufs = Smem::kBufs, kQBufs = Smem::kQBufs, kHalves = D / 128;
+    constexpr bool kTwo = Smem::kTwo;
+    constexpr int kQ = kTwo ? kQWarps - 1 : kQWarps;  // warps that split q
     constexpr uint32_t kHalfBytes = kN * 128;
     constexpr int kPart = kM * D + 2 * kM;
     extern __shared__ uint8_t smem_raw[];
@@ -250,17 +253,17 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
         }
         for (int i = 0; i < kBufs; ++i) {
             tc::mbar_init(s_full + 8 * i, 1);
+            tc::mbar_init(o_done + 8 * i, 1);
             tc::mbar_init(p_ready + 8 * i, kTeamWarps);
         }
         for (int i = 0; i < kScaleRing; ++i) tc::mbar_init(scales_full + 8 * i, 1);
         for (int i = 0; i < kQBufs; ++i) {
-            tc::mbar_init(q_full + 8 * i, kQWarps);
+            tc::mbar_init(q_full + 8 * i, kQ);
             tc::mbar_init(q_empty + 8 * i, 1 + kSoftWarps);
         }
-        for (int i = 0; i < 2; ++i) tc::mbar_init(o_done + 8 * i, 1);
         tc::mbar_init(o_free, kSoftWarps);
         tc::mbar_init(item_done, 1);
-        tc::mbar_init(drained, 1);
+        tc::mbar_init(drained, kTwo ? 2 : 1);
     }
     if (warp == kMmaWarp) tc::tmem_alloc(tc::smem_u32(&sm.tmem), 512);
     tc::fence_before_sync();
@@ -348,77 +351,98 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
         }
         // Copies that nobody waited for (after a wait that gave up) land before the CTA ends.
         for (int i = max(0, issued - kSlots); i < issued; ++i) tc::mbar_wait(full + 8 * (i % kSlots), (i / kSlots) & 1, kDrainNs);
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kMmaWarp || (kTwo && warp == kMmaWarp2)) {
         // ------------------------------------------------------------- MMAs
-        // The whole warp walks and waits; one elected lane issues.  (An MMA takes
-        // its descriptors from uniform registers: under a test of the lane number
+        // A whole warp walks and waits; one elected lane issues.  (An MMA takes its
+        // descriptors from uniform registers: under a test of the lane number
         // instead, each one costs about 185 cycles of issue, three times its own 64.)
+        // Beside the softmax a tile's issue takes about 850 cycles a product.  For
+        // d = 256, where the products take 1,024 each, one warp issues both, and the
+        // tensor pipe's order keeps a tile's weights until their product has read
+        // them; for d = 128 (512 each) a warp for each, the logits' one waiting for that product.
         constexpr uint32_t id_s = tc::idesc_e4m3(kM, kN, false), id_o = tc::idesc_e4m3(kM, D, true);
         const uint32_t ring = tc::smem_u32(sm.ring[0]);
-        int gs = 0, gp = 0;                       // tiles whose logits, whose product have been issued
-        uint32_t firsts = 0, lasts = 0;           // of the items, by tile modulo 32
-        int item = 0, item_p = 0;
-        auto product = [&]() {
-            const int u = 2 * gp + 1, slot = u % kSlots, buf = gp % kBufs;
-            const bool first = (firsts >> (gp & 31)) & 1, last = (lasts >> (gp & 31)) & 1;
-            if (first && item_p > 0) wait(o_free, item_p - 1);
+        auto logits = [&](int g, int qb, bool last) {
+            const int u = 2 * g, slot = u % kSlots, buf = g % kBufs;
             wait(full + 8 * slot, u / kSlots);
-            wait(p_ready + 8 * buf, gp / kBufs);
-            {
-                tc::fence_after_sync();
-                const uint64_t v = tc::smem_desc_mn_sw128(ring + slot * kSlot, kHalfBytes);
-                const uint32_t a = tmem + buf * kN;
-                if (tc::elect_one()) {
-#pragma unroll
-                    for (int part = 0; part < 2; ++part)
-#pragma unroll
-                        for (int ks = 0; ks < kN / 32; ++ks)
-                            tc::mma_e4m3_ts(tO, a + (ks >> 1) * 64 + (ks & 1) * 8 + part * 16, v + (ks * 32 * 128 >> 4), id_o, part + ks > 0 || !first);
-                    tc::mma_commit(empty + 8 * slot);
-                    tc::mma_commit(o_done + 8 * (gp & 1));
-                    if (last) tc::mma_commit(item_done);
-                }
-                __syncwarp();
-            }
-            if (last) ++item_p;
-            ++gp;
-        };
-        for (; w.settle(p); w.advance(p), ++item) {
-            const int qb = item % kQBufs;
-            // the products that are due first, unless this item's q is there already
-            if (!__all_sync(~0u, tc::mbar_test(q_full + 8 * qb, (item / kQBufs) & 1)))
-                while (gp < gs) product();
-            wait(q_full + 8 * qb, item / kQBufs);
+            tc::fence_after_sync();
             const uint64_t q_hi = tc::smem_desc_sw128(tc::smem_u32(sm.q[0][0]) + qb * 2 * kM * D), q_lo = q_hi + (kM * D >> 4);
-            for (int j = w.j0; j < w.j1; ++j) {
-                while (gp <= gs - kBufs) product();  // the buffer's last reader
-                const int u = 2 * gs, slot = u % kSlots, buf = gs % kBufs;
-                wait(full + 8 * slot, u / kSlots);
-                {
-                    tc::fence_after_sync();
-                    const uint64_t k = tc::smem_desc_sw128(ring + slot * kSlot);
-                    const uint32_t d = tmem + buf * kN;
-                    if (tc::elect_one()) {
+            const uint64_t k = tc::smem_desc_sw128(ring + slot * kSlot);
+            const uint32_t d = tmem + buf * kN;
+            if (tc::elect_one()) {
 #pragma unroll
-                        for (int part = 0; part < 2; ++part)
+                for (int part = 0; part < 2; ++part)
 #pragma unroll
-                            for (int ks = 0; ks < D / 32; ++ks) {
-                                const uint32_t at = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
-                                tc::mma_e4m3(d, (part ? q_lo : q_hi) + at, k + at, id_s, part + ks > 0);
-                            }
-                        tc::mma_commit(empty + 8 * slot);
-                        tc::mma_commit(s_full + 8 * buf);
-                        if (j == w.j1 - 1) tc::mma_commit(q_empty + 8 * qb);
+                    for (int ks = 0; ks < D / 32; ++ks) {
+                        const uint32_t at = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
+                        tc::mma_e4m3(d, (part ? q_lo : q_hi) + at, k + at, id_s, part + ks > 0);
                     }
-                    __syncwarp();
-                }
-                const uint32_t bit = 1u << (gs & 31);
-                firsts = j == w.j0 ? firsts | bit : firsts & ~bit;
-                lasts = j == w.j1 - 1 ? lasts | bit : lasts & ~bit;
-                ++gs;
+                tc::mma_commit(empty + 8 * slot);
+                tc::mma_commit(s_full + 8 * buf);
+                if (last) tc::mma_commit(q_empty + 8 * qb);
             }
+            __syncwarp();
+        };
+        auto product = [&](int g, int item, bool first, bool last) {
+            const int u = 2 * g + 1, slot = u % kSlots, buf = g % kBufs;
+            if (first && item > 0) wait(o_free, item - 1);
+            wait(full + 8 * slot, u / kSlots);
+            wait(p_ready + 8 * buf, g / kBufs);
+            tc::fence_after_sync();
+            const uint64_t v = tc::smem_desc_mn_sw128(ring + slot * kSlot, kHalfBytes);
+            const uint32_t a = tmem + buf * kN;
+            if (tc::elect_one()) {
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int ks = 0; ks < kN / 32; ++ks)
+                        tc::mma_e4m3_ts(tO, a + (ks >> 1) * 64 + (ks & 1) * 8 + part * 16, v + (ks * 32 * 128 >> 4), id_o, part + ks > 0 || !first);
+                tc::mma_commit(empty + 8 * slot);
+                tc::mma_commit(o_done + 8 * buf);
+                if (last) tc::mma_commit(item_done);
+            }
+            __syncwarp();
+        };
+        if constexpr (kTwo) {
+            int g = 0, item = 0;
+            for (; w.settle(p); w.advance(p), ++item) {
+                if (warp == kMmaWarp) wait(q_full + 8 * (item % kQBufs), item / kQBufs);
+                for (int j = w.j0; j < w.j1; ++j, ++g) {
+                    if (warp == kMmaWarp) {
+                        if (g >= kBufs) wait(o_done + 8 * (g % kBufs), g / kBufs - 1);
+                        logits(g, item % kQBufs, j == w.j1 - 1);
+                    } else {
+                        product(g, item, j == w.j0, j == w.j1 - 1);
+                    }
+                }
+            }
+        } else {
+            int gs = 0, gp = 0;                   // tiles whose logits, whose product have been issued
+            uint32_t firsts = 0, lasts = 0;       // of the items, by tile modulo 32
+            int item = 0, item_p = 0;
+            auto product_next = [&]() {
+                const bool last = (lasts >> (gp & 31)) & 1;
+                product(gp, item_p, (firsts >> (gp & 31)) & 1, last);
+                if (last) ++item_p;
+                ++gp;
+            };
+            for (; w.settle(p); w.advance(p), ++item) {
+                const int qb = item % kQBufs;
+                // the products that are due first, unless this item's q is there already
+                if (!__all_sync(~0u, tc::mbar_test(q_full + 8 * qb, (item / kQBufs) & 1)))
+                    while (gp < gs) product_next();
+                wait(q_full + 8 * qb, item / kQBufs);
+                for (int j = w.j0; j < w.j1; ++j) {
+                    while (gp <= gs - kBufs) product_next();  // the buffer's last reader
+                    logits(gs, qb, j == w.j1 - 1);
+                    const uint32_t bit = 1u << (gs & 31);
+                    firsts = j == w.j0 ? firsts | bit : firsts & ~bit;
+                    lasts = j == w.j1 - 1 ? lasts | bit : lasts & ~bit;
+                    ++gs;
+                }
+            }
+            while (gp < gs) product_next();
         }
-        while (gp < gs) product();
         // every MMA has ended before tensor memory is given back
         if (tc::elect_one()) tc::mma_commit(drained);
         __syncwarp();
@@ -434,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
             const int rows_next = w.r.n * p.G - w.t * kM;
             const RowMap map_next(p, w.t);
 #pragma unroll 1
-            for (int i = (warp - kQWarp0) * 32 + lane; i < kM * (D / 64); i += kQWarps * 32) {
+            for (int i = (warp - kQWarp0) * 32 + lane; i < kM * (D / 64); i += kQ * 32) {
                 const int local = i / (D / 64);
                 if (local < rows_next) {
                     int qi, hg;
@@ -451,11 +475,11 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
             const int qb = item % kQBufs;
             bool waited = item < kQBufs;
 #pragma unroll 1
-            for (int i0 = warp - kQWarp0; i0 < kM / kAtOnce; i0 += kBatch * kQWarps) {
+            for (int i0 = warp - kQWarp0; i0 < kM / kAtOnce; i0 += kBatch * kQ) {
                 uint4 x[kBatch][2];
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                    const int local = (i0 + i * kQWarps) * kAtOnce + sub;
+                    const int local = (i0 + i * kQ) * kAtOnce + sub;
                     x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
                     if (local < min(rows, kM)) {
                         int qi, hg;
@@ -469,8 +493,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                 waited = true;
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                    const int local = (i0 + i * kQWarps) * kAtOnce + sub;
-                    if (i0 + i * kQWarps >= kM / kAtOnce) break;  // uniform in the warp
+                    const int local = (i0 + i * kQ) * kAtOnce + sub;
+                    if (i0 + i * kQ >= kM / kAtOnce) break;  // uniform in the warp
                     const uint32_t word[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
                     uint32_t m2 = 0;
 #pragma unroll
@@ -600,9 +624,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                     l *= factor(m, ref);
                     m = ref;
                     if (j > w.j0 && __any_sync(~0u, grows)) {
-                        // This tile's logits came after product g - 2, and product g waits for this team: the barrier
-                        // is in the phase of product g - 1 or just past it, which its parity tells apart.
-                        wait(o_done + 8 * (team ^ 1), (g - 1) >> 1);
+                        // This tile's logits came after product g - kBufs, and product g waits for this team: the
+                        // barrier is in the phase of product g - 1 or just past it, which its parity tells apart.
+                        wait(o_done + 8 * ((g - 1) % kBufs), (g - 1) / kBufs);
                         tc::fence_after_sync();
                         const float c = grows ? ex2(old - ref) : 1.0f;
 #pragma unroll 1
