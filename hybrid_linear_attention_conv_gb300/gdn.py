@@ -9,6 +9,7 @@ error.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -104,6 +105,8 @@ _lib = None
 def load(path: str = LIB_PATH):
     """Load the shared library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -179,6 +182,11 @@ def _shape(B, Hk, Hv, dk, dv) -> gdn_shape:
 
 def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+def _raw_stream() -> int:
+    """The current stream's handle, without the Stream object around it."""
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _dev(t: torch.Tensor | None, dtype, name: str, shape=None):
@@ -757,28 +765,46 @@ KV_PLAN_STATUS = {1: "the free pages do not suffice", 2: "a request outgrows its
                   4: "more new tokens than rows", 8: "a negative or inconsistent count"}
 
 
-def _rows3(t: torch.Tensor, name: str, heads=None, d=None) -> tuple[ctypes.c_void_p, int]:
+def _ptr(t, dtype, name: str, shape) -> int:
+    """_dev for the step's calls, where a microsecond counts: the same checks, a plain address."""
+    if t is None:
+        return 0
+    try:
+        if t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _dev(t, dtype, name, shape).value or 0
+
+
+@functools.lru_cache(maxsize=256)
+def _kv_shape(B, Hq, Hkv, d, page, pages, width):
+    return ctypes.byref(gdn_kv_shape(B, Hq, Hkv, d, page, pages, width))
+
+
+def _rows3(t: torch.Tensor, name: str, heads=None, d=None) -> tuple[int, int]:
     """A bf16 CUDA tensor [rows, heads, d] whose rows may be strided apart but are
-    each contiguous: (pointer, row stride in elements)."""
+    each contiguous: (address, row stride in elements)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3 or (heads is not None and tuple(t.shape[1:]) != (heads, d)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (rows, {heads or 'heads'}, {d or 'd'})")
-    if (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    shape = t.shape
+    if len(shape) != 3 or (heads is not None and (shape[1] != heads or shape[2] != d)):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected (rows, {heads or 'heads'}, {d or 'd'})")
+    s0, s1, s2 = t.stride()
+    if (shape[2] > 1 and s2 != 1) or (shape[1] > 1 and s1 != shape[2]):
         raise ValueError(f"each row of {name} must be contiguous")
-    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-    return ctypes.c_void_p(t.data_ptr()), int(ld)
+    return t.data_ptr(), s0 if shape[0] > 1 else shape[1] * shape[2]
 
 
 def _kv_cache(k_cache, v_cache, k_scale, v_scale):
-    """Pointers of a cache: codes float8_e4m3fn [pages,Hkv,page,d], scales fp32 [pages,Hkv]."""
+    """Addresses of a cache: codes float8_e4m3fn [pages,Hkv,page,d], scales fp32 [pages,Hkv]."""
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache must be a tensor [pages, Hkv, page, d]")
-    shape = tuple(k_cache.shape)
-    return (_dev(k_cache, torch.float8_e4m3fn, "k_cache"), _dev(v_cache, torch.float8_e4m3fn, "v_cache", shape),
-            _dev(k_scale, torch.float32, "k_scale", shape[:2]), _dev(v_scale, torch.float32, "v_scale", shape[:2]))
+    shape = k_cache.shape
+    return (_ptr(k_cache, torch.float8_e4m3fn, "k_cache", shape), _ptr(v_cache, torch.float8_e4m3fn, "v_cache", shape),
+            _ptr(k_scale, torch.float32, "k_scale", shape[:2]), _ptr(v_scale, torch.float32, "v_scale", shape[:2]))
 
 
 def kv_plan(lens, new, held, free_pages, free_count, table, page, rows, out=None):
@@ -787,18 +813,19 @@ def kv_plan(lens, new, held, free_pages, free_count, table, page, rows, out=None
     tokens a page, rows: the step's tokens (or more).  Returns (lens, held, free_count, start
     [B+1], slots int64 [rows], status [1]), or fills the tuple `out`; kv_plan_check reads status."""
     B, width = table.shape
-    i32 = torch.int32
+    i32, b1, one = torch.int32, (B,), (1,)
     if out is None:
-        e = lambda n, dt=i32: torch.empty(n, dtype=dt, device=table.device)  # noqa: E731
-        out = (e(B), e(B), e(1), e(B + 1), e(rows, torch.int64), e(1))
-    shapes = ((B,), (B,), (1,), (B + 1,), (rows,), (1,))
-    names = ("lens_out", "held_out", "free_count_out", "start", "slots", "status")
-    ptrs = [_dev(t, torch.int64 if n == "slots" else i32, n, sh) for t, n, sh in zip(out, names, shapes)]
-    sh = gdn_kv_shape(B, 1, 1, 128, int(page), 0, width)
-    rc = load().gdn_kv_plan(ctypes.byref(sh), _dev(lens, i32, "lens", (B,)), _dev(new, i32, "new", (B,)),
-                            _dev(held, i32, "held", (B,)), _dev(free_pages, i32, "free_pages"), free_pages.numel(),
-                            _dev(free_count, i32, "free_count", (1,)), _dev(table, i32, "table"), int(rows), *ptrs, _stream())
-    _check(rc, "gdn_kv_plan")
+        e, dev = torch.empty, table.device
+        out = (e(b1, dtype=i32, device=dev), e(b1, dtype=i32, device=dev), e(one, dtype=i32, device=dev),
+               e((B + 1,), dtype=i32, device=dev), e((rows,), dtype=torch.int64, device=dev), e(one, dtype=i32, device=dev))
+    rc = load().gdn_kv_plan(_kv_shape(B, 1, 1, 128, int(page), 0, width), _ptr(lens, i32, "lens", b1), _ptr(new, i32, "new", b1),
+                            _ptr(held, i32, "held", b1), _ptr(free_pages, i32, "free_pages", (free_pages.numel(),)), free_pages.numel(),
+                            _ptr(free_count, i32, "free_count", one), _ptr(table, i32, "table", (B, width)), int(rows),
+                            _ptr(out[0], i32, "lens_out", b1), _ptr(out[1], i32, "held_out", b1), _ptr(out[2], i32, "free_count_out", one),
+                            _ptr(out[3], i32, "start", (B + 1,)), _ptr(out[4], torch.int64, "slots", (rows,)), _ptr(out[5], i32, "status", one),
+                            _raw_stream())
+    if rc:
+        _check(rc, "gdn_kv_plan")
     return out
 
 
@@ -818,12 +845,13 @@ def kv_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, rows=None) -> Non
     T = slots.numel()
     kp, ldk = _rows3(k, "k", Hkv, d)
     vp, ldv = _rows3(v, "v", Hkv, d)
-    if k.shape[0] != v.shape[0]:
-        raise ValueError(f"k has {k.shape[0]} rows, v has {v.shape[0]}")
-    sh = gdn_kv_shape(1, Hkv, Hkv, d, page, pages, 0)
-    rc = load().gdn_kv_append(ctypes.byref(sh), T, kp, ldk, vp, ldv, k.shape[0], _dev(slots, torch.int64, "slots", (T,)),
-                              _dev(rows, torch.int32, "rows", (T,)), *cache, _stream())
-    _check(rc, "gdn_kv_append")
+    n = k.shape[0]
+    if v.shape[0] != n:
+        raise ValueError(f"k has {n} rows, v has {v.shape[0]}")
+    rc = load().gdn_kv_append(_kv_shape(1, Hkv, Hkv, d, page, pages, 0), T, kp, ldk, vp, ldv, n, _ptr(slots, torch.int64, "slots", (T,)),
+                              _ptr(rows, torch.int32, "rows", (T,)), *cache, _raw_stream())
+    if rc:
+        _check(rc, "gdn_kv_append")
 
 
 def kv_attention_workspace_bytes(Hq, Hkv, d) -> int:
@@ -846,15 +874,17 @@ def kv_attention(q, k_cache, v_cache, k_scale, v_scale, table, start, lens, scal
     B, width = table.shape
     if out is None:
         out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=q.device)
-    sh = gdn_kv_shape(B, Hq, Hkv, d, page, pages, width)
+    sh = _kv_shape(B, Hq, Hkv, d, page, pages, width)
     if workspace is None:
-        workspace = torch.zeros(max(int(load().gdn_kv_attention_workspace_bytes(ctypes.byref(sh))), 1), dtype=torch.uint8, device=q.device)
-    rc = load().gdn_kv_attention(ctypes.byref(sh), T, qp, ldq, *cache, _dev(table, torch.int32, "table"),
-                                 _dev(start, torch.int32, "start", (B + 1,)), _dev(lens, torch.int32, "lens", (B,)),
-                                 _dev(tree, torch.int64, "tree", (T,)), float(d ** -0.5 if scale is None else scale),
-                                 _dev(out, torch.bfloat16, "out", (T, Hq, d)), _dev(lse, torch.float32, "lse", (T, Hq)),
-                                 _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream())
-    _check(rc, "gdn_kv_attention")
+        workspace = torch.zeros(max(int(load().gdn_kv_attention_workspace_bytes(sh)), 1), dtype=torch.uint8, device=q.device)
+    i32, size = torch.int32, workspace.numel()
+    rc = load().gdn_kv_attention(sh, T, qp, ldq, *cache, _ptr(table, i32, "table", (B, width)), _ptr(start, i32, "start", (B + 1,)),
+                                 _ptr(lens, i32, "lens", (B,)), _ptr(tree, torch.int64, "tree", (T,)),
+                                 d ** -0.5 if scale is None else scale, _ptr(out, torch.bfloat16, "out", (T, Hq, d)),
+                                 _ptr(lse, torch.float32, "lse", (T, Hq)), _ptr(workspace, torch.uint8, "workspace", (size,)), size,
+                                 _raw_stream())
+    if rc:
+        _check(rc, "gdn_kv_attention")
     return out
 
 
