@@ -51,7 +51,8 @@ constexpr int kRows = 8;
 constexpr int kRingBytes = 24 * 1024;   // a warp's ring: 3 units of 8 KB or 6 of 4 KB
 constexpr float kPScale = 8.0f;         // weights are held times 2^8: e4m3 reaches 448
 constexpr uint64_t kDrainNs = 200000000ull;
-constexpr int kMinTiles = 8;            // tiles a CTA takes at least
+constexpr int kItemCost = 8;            // an item's beginning and end, in tiles
+constexpr int kMinTiles = 16;           // what a CTA takes at least
 
 template <int D>
 struct RowsSmem {
@@ -65,11 +66,14 @@ struct RowsSmem {
     unsigned last;
 };
 
-// A request's part of the list of tiles.
+// A request's part of the list of tiles.  An item (head, row block) takes
+// kItemCost places of the list before its tiles' own, so that CTAs with many
+// short items get fewer tiles.
 struct Request {
     int n, L, row0;        // queries, tokens, first row of q
     int row_blocks, tiles; // of eight rows; of 32 tokens (at least one)
-    long long work;        // row_blocks * Hkv * tiles
+    int items;             // row_blocks * Hkv
+    long long work;        // items * (tiles + kItemCost)
 };
 
 __device__ __forceinline__ Request request(const KvAttnParams& p, int b) {
@@ -80,21 +84,16 @@ __device__ __forceinline__ Request request(const KvAttnParams& p, int b) {
     r.L = max(0, min(p.lens[b], p.width << p.log2_page));
     r.row_blocks = (r.n * p.G + kRows - 1) / kRows;
     r.tiles = max(1, (r.L + kTile - 1) / kTile);
-    r.work = (long long)r.row_blocks * p.Hkv * r.tiles;
+    r.items = r.row_blocks * p.Hkv;
+    r.work = (long long)r.items * (r.tiles + kItemCost);
     return r;
 }
 
 __device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-    return v;
 }
 
 // Bytes of four tokens (words r0..r3, four columns each) to four columns of
@@ -128,7 +127,8 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_kv_attn_rows_kernel(const __g
     extern __shared__ uint8_t smem_raw[];
     RowsSmem<D>& sm = *reinterpret_cast<RowsSmem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
-    const uint32_t ring = tc::smem_u32(sm.ring[warp]), bars = tc::smem_u32(sm.full[warp]);
+    const uint8_t* ring = sm.ring[warp];
+    const uint32_t ring_at = tc::smem_u32(ring), bars = tc::smem_u32(sm.full[warp]);
     if (lane == 0)
         for (int i = 0; i < kUnits; ++i) tc::mbar_init(bars + 8 * i, 1);
 
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_kv_attn_rows_kernel(const __g
         if (w < warp) upto += sm.scan[w];
         total += sm.scan[w];
     }
-    const long long W = max((total + gridDim.x - 1) / gridDim.x, (long long)kMinTiles);
+    const long long W = max((total + gridDim.x - 1) / gridDim.x, (long long)kMinTiles);  // places a CTA
     const long long x0 = blockIdx.x * W, x1 = min(x0 + W, total);
     if (x0 >= x1) return;  // uniform; nothing is in flight
     if (upto - mine <= x0 && x0 < upto) {
@@ -167,71 +167,86 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_kv_attn_rows_kernel(const __g
         sm.at_rest = rest;
     }
     __syncthreads();
-    int b = sm.at_b;
-    long long rest = sm.at_rest;  // tiles of request b before x
-    long long x = x0;
     int slot = 0;                 // ring position and parity of the next unit to be read,
     uint32_t parity = 0;
     int islot = 0;                // and position of the next to be filled
 
-    while (x < x1) {
-        const Request r = request(p, b);
-        if (rest >= r.work) {  // also a request without queries
-            rest -= r.work;
-            ++b;
-            continue;
+    // The stretch at hand: request b's item `item`, tiles t0 .. t1 - 1; x is the
+    // place of the list that its place v0 lies at.
+    int b = sm.at_b;
+    Request r = request(p, b);
+    int item = (int)(sm.at_rest / (r.tiles + kItemCost)), v0 = (int)(sm.at_rest - (long long)item * (r.tiles + kItemCost));
+    int t0 = 0, t1 = 0;
+    long long x = x0;
+    auto settle = [&]() {  // false: the CTA's part is done
+        while (x < x1) {
+            if (item >= r.items) {
+                r = request(p, ++b);
+                item = 0;
+                continue;
+            }
+            const int v1 = (int)min((long long)r.tiles + kItemCost, v0 + (x1 - x));
+            t0 = max(0, v0 - kItemCost);
+            t1 = max(0, v1 - kItemCost);
+            if (t0 < t1) return true;
+            x += v1 - v0;
+            v0 = 0;
+            ++item;
         }
-        const int item = (int)(rest / r.tiles), t0 = (int)(rest - (long long)item * r.tiles);
-        const int t1 = (int)min((long long)r.tiles, t0 + (x1 - x));
-        const int h = item % p.Hkv, block = item / p.Hkv;
+        return false;
+    };
+    // This warp's tiles of it: t0 + warp + 4 i, i < nt.  32 tiles' places and
+    // scales at a time, a lane each; the ones looked up last, and the ones in use.
+    int nt = 0, h = 0, yI = 0;
+    float ksI = 0.0f, vsI = 1.0f, ksC = 0.0f, vsC = 1.0f;
+    auto lookup = [&](int i0) {
+        const int i = i0 + lane;
+        if (i < nt) {
+            const int pos = (t0 + warp + kWarps * i) * kTile;
+            const int idx = pos >> p.log2_page;
+            const int page = idx < p.width ? p.table[(int64_t)b * p.width + idx] : -1;
+            const bool good = page >= 0 && page < p.pages;
+            yI = cache_row(page, p.pages, p.Hkv, h, p.log2_page, pos);
+            ksI = good ? p.k_scale[(int64_t)page * p.Hkv + h] : __int_as_float(0x7fffffff);
+            vsI = good ? p.v_scale[(int64_t)page * p.Hkv + h] : __int_as_float(0x7fffffff);
+        }
+    };
+    int issued = 0;  // units
+    auto issue = [&]() {
+        if (issued >= 2 * nt) return;
+        const int i = issued >> 1;
+        if ((issued & 63) == 0) lookup(i);
+        const int y = __shfl_sync(~0u, yI, i & 31);
+        if (lane == 0) {
+            const void* map = (issued & 1) ? &p.tm_v : &p.tm_k;
+            tc::mbar_arrive_expect_tx(bars + 8 * islot, kUnit);
+#pragma unroll
+            for (int hf = 0; hf < kHalves; ++hf)
+                tc::tma_load_2d(ring_at + islot * kUnit + hf * (kTile * 128), map, hf * 128, y, bars + 8 * islot);
+        }
+        islot = islot + 1 == kUnits ? 0 : islot + 1;
+        ++issued;
+    };
+    auto begin = [&]() {  // the stretch's first copies
+        nt = t1 - t0 > warp ? (t1 - t0 - warp + kWarps - 1) / kWarps : 0;
+        h = item % p.Hkv;
+        issued = 0;
+        for (int i = 0; i < kUnits; ++i) issue();
+    };
+
+    bool more = settle();
+    if (more) begin();
+    while (more) {
         // rows of this block: row -> query i, head of the group
-        const int row = block * kRows + g;
+        const int block = item / p.Hkv, row = block * kRows + g;
         const bool have = row < r.n * p.G;
         const int qi = have ? row / p.G : 0, head = h * p.G + (have ? row - qi * p.G : 0);
         const int base = r.L - r.n;                     // tokens that every query sees
         const int seen = have ? base + qi + 1 : 0;      // causal: tokens below this
         const unsigned long long tree = p.tree != nullptr && have ? (unsigned long long)p.tree[r.row0 + qi] : 0ull;
         const int all_see = max(0, min(r.L, p.tree != nullptr ? base : base + (block * kRows) / p.G + 1));
-
-        const int nt = t1 - t0 > warp ? (t1 - t0 - warp + kWarps - 1) / kWarps : 0;  // this warp's tiles t0 + warp + 4 i
-        // 32 tiles' places and scales at a time, a lane each
-        int yI = 0;
-        float ksI = 0.0f, lvI = 0.0f, ksC = 0.0f, lvC = 0.0f;
-        auto lookup = [&](int i0) {
-            const int i = i0 + lane;
-            if (i < nt) {
-                const int pos = (t0 + warp + kWarps * i) * kTile;
-                const int idx = pos >> p.log2_page;
-                const int page = idx < p.width ? p.table[(int64_t)b * p.width + idx] : -1;
-                const bool good = page >= 0 && page < p.pages;
-                yI = cache_row(page, p.pages, p.Hkv, h, p.log2_page, pos);
-                ksI = good ? p.k_scale[(int64_t)page * p.Hkv + h] : __int_as_float(0x7fffffff);
-                lvI = good ? log2f(p.v_scale[(int64_t)page * p.Hkv + h]) : __int_as_float(0x7fffffff);
-            }
-        };
-        int issued = 0;  // units
-        auto issue = [&]() {
-            if (issued >= 2 * nt) return;
-            const int i = issued >> 1;
-            if ((issued & 63) == 0) lookup(i);
-            const int y = __shfl_sync(~0u, yI, i & 31);
-            if (lane == 0) {
-                const void* map = (issued & 1) ? &p.tm_v : &p.tm_k;
-                tc::mbar_arrive_expect_tx(bars + 8 * islot, kUnit);
-#pragma unroll
-                for (int hf = 0; hf < kHalves; ++hf)
-                    tc::tma_load_2d(ring + islot * kUnit + hf * (kTile * 128), map, hf * 128, y, bars + 8 * islot);
-            }
-            islot = islot + 1 == kUnits ? 0 : islot + 1;
-            ++issued;
-        };
-        for (int i = 0; i < kUnits; ++i) {
-            issue();
-            if (i == 0) {
-                ksC = ksI;
-                lvC = lvI;
-            }
-        }
+        ksC = ksI;
+        vsC = vsI;
 
         // q as hi + lo, times a power of two that brings its largest to (224, 448]
         uint32_t qa[kHalves * 4][4];
@@ -298,9 +313,9 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_kv_attn_rows_kernel(const __g
             const int pos0 = (t0 + warp + kWarps * i) * kTile;
             if ((i & 31) == 0 && i > 0) {
                 ksC = ksI;
-                lvC = lvI;
+                vsC = vsI;
             }
-            const float ks = __shfl_sync(~0u, ksC, i & 31), lv = __shfl_sync(~0u, lvC, i & 31);
+            const float ks = __shfl_sync(~0u, ksC, i & 31), vs = __shfl_sync(~0u, vsC, i & 31), lv = __log2f(vs);
             // ---- logits
             wait_unit();
             float s[4][4];
@@ -309,13 +324,15 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_kv_attn_rows_kernel(const __g
 #pragma unroll
             for (int hf = 0; hf < kHalves; ++hf)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t rowa = ring + slot * kUnit + hf * (kTile * 128) + (8 * j + g) * 128;
-                    const uint4 c0 = lds128(rowa + (((2 * q4) ^ g) << 4)), c1 = lds128(rowa + (((2 * q4 + 1) ^ g) << 4));
-                    mma_e4m3(s[j], qa[hf * 4 + 0], c0.x, c0.y);
-                    mma_e4m3(s[j], qa[hf * 4 + 1], c0.z, c0.w);
-                    mma_e4m3(s[j], qa[hf * 4 + 2], c1.x, c1.y);
-                    mma_e4m3(s[j], qa[hf * 4 + 3], c1.z, c1.w);
+                for (int cc = 0; cc < 2; ++cc) {  // four accumulators at a time: an MMA's result is 22 cycles away
+                    uint4 k[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        k[j] = *reinterpret_cast<const uint4*>(ring + slot * kUnit + hf * (kTile * 128) + (8 * j + g) * 128 + (((2 * q4 + cc) ^ g) << 4));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mma_e4m3(s[j], qa[hf * 4 + 2 * cc], k[j].x, k[j].y);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mma_e4m3(s[j], qa[hf * 4 + 2 * cc + 1], k[j].z, k[j].w);
                 }
             next_unit();
             // ---- weights
@@ -361,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_kv_attn_rows_kernel(const __g
                 w[k] = ex2(t[k] + shift);  // a token that is not seen: 2^-inf = 0
                 sum += w[k];
             }
-            if (sum != 0.0f) l = fmaf(sum, ex2(-lv), l);  // a row that sees nothing here takes nothing from the block's scale
+            if (sum != 0.0f) l = fmaf(sum, __fdividef(1.0f, vs), l);  // a row that sees nothing here takes nothing from the block's scale
             uint32_t pa[4];
             {
                 split4_f16(w[0], w[1], w[2], w[3], pa[0], pa[1]);
@@ -376,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_kv_attn_rows_kernel(const __g
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const int tok = 8 * (k >> 1) + 2 * q4 + (k & 1);
-                    v[k] = lds128(ring + slot * kUnit + hf * (kTile * 128) + tok * 128 + ((g ^ (tok & 7)) << 4));
+                    v[k] = *reinterpret_cast<const uint4*>(ring + slot * kUnit + hf * (kTile * 128) + tok * 128 + ((g ^ (tok & 7)) << 4));
                     if (tail && pos0 + tok >= r.L) v[k] = make_uint4(0, 0, 0, 0);  // whatever lies past the end
                 }
 #pragma unroll
@@ -392,6 +409,17 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_kv_attn_rows_kernel(const __g
         }
         l += __shfl_xor_sync(~0u, l, 1);
         l += __shfl_xor_sync(~0u, l, 2);
+
+        // ---- the next stretch's copies go out before this one's output is put together
+        const long long tile0 = x - v0 + kItemCost;  // the place of the item's first tile
+        const int c0 = (int)(tile0 / W), c1 = (int)((tile0 + r.tiles - 1) / W);
+        const bool from_start = t0 == 0;
+        const int64_t at = (int64_t)(r.row0 + qi) * p.Hq + head;
+        x += t1 + kItemCost - v0;
+        v0 = 0;
+        ++item;
+        more = settle();
+        if (more) begin();
 
         // ---- the four warps' states into warp 0's, one after another
         float acc[kHalves * 16][2];
@@ -435,12 +463,10 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_kv_attn_rows_kernel(const __g
 
         // ---- the whole item here: write it; else leave a part, and the last
         // CTA of the item joins them all
-        const long long item0 = x - t0, item1 = item0 + r.tiles;
-        const int c0 = (int)(item0 / W), c1 = (int)((item1 - 1) / W);
         bool write = warp == 0;
         constexpr int kPart = kRows * D + 2 * kRows;
         if (c0 != c1) {
-            float* part = p.partials + ((size_t)blockIdx.x * 2 + (t0 == 0 ? 1 : 0)) * kPart;
+            float* part = p.partials + ((size_t)blockIdx.x * 2 + (from_start ? 1 : 0)) * kPart;
             if (warp == 0) {
                 give(part);
                 if (q4 == 0) {
@@ -476,7 +502,6 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_kv_attn_rows_kernel(const __g
         if (write && have) {
             const bool empty = l == 0.0f;  // no token seen: zeros
             const float inv = empty ? 0.0f : 1.0f / l;
-            const int64_t at = (int64_t)(r.row0 + qi) * p.Hq + head;
 #pragma unroll
             for (int hf = 0; hf < kHalves; ++hf) {
                 uint16_t* dst = p.out + at * D + hf * 128 + 32 * q4;
@@ -494,9 +519,6 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_kv_attn_rows_kernel(const __g
             if (p.lse != nullptr && q4 == 0)
                 p.lse[at] = empty ? -INFINITY : ((m == -INFINITY ? 0.0f : m) - kPScale + log2f(l)) * 0.69314718055994531f;
         }
-        const int done = t1 - t0;
-        x += done;
-        rest += done;
     }
 }
 
