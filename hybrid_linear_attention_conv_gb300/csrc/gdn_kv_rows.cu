@@ -39,6 +39,7 @@
 #include <mutex>
 
 #include "gdn_kv.cuh"
+#include "gdn_kv_tc.cuh"
 #include "gdn_tc.cuh"
 
 namespace gdn {
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_kv_attn_rows_kernel(const __g
         const int i = issued >> 1;
         if ((issued & 63) == 0) lookup(i);
         const int y = __shfl_sync(~0u, yI, i & 31);
-        if (lane == 0) {
+        if (tc::elect_one()) {  // (a copy's operands are uniform registers: not under a test of the lane number)
             const void* map = (issued & 1) ? &p.tm_v : &p.tm_k;
             tc::mbar_arrive_expect_tx(bars + 8 * islot, kUnit);
 #pragma unroll
@@ -324,16 +325,13 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_kv_attn_rows_kernel(const __g
 #pragma unroll
             for (int hf = 0; hf < kHalves; ++hf)
 #pragma unroll
-                for (int cc = 0; cc < 2; ++cc) {  // four accumulators at a time: an MMA's result is 22 cycles away
-                    uint4 k[4];
+                for (int cc = 0; cc < 2; ++cc)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        k[j] = *reinterpret_cast<const uint4*>(ring + slot * kUnit + hf * (kTile * 128) + (8 * j + g) * 128 + (((2 * q4 + cc) ^ g) << 4));
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) mma_e4m3(s[j], qa[hf * 4 + 2 * cc], k[j].x, k[j].y);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) mma_e4m3(s[j], qa[hf * 4 + 2 * cc + 1], k[j].z, k[j].w);
-                }
+                    for (int j = 0; j < 4; ++j) {  // four accumulators in turn: an MMA's result is 22 cycles away
+                        const uint4 k = *reinterpret_cast<const uint4*>(ring + slot * kUnit + hf * (kTile * 128) + (8 * j + g) * 128 + (((2 * q4 + cc) ^ g) << 4));
+                        mma_e4m3(s[j], qa[hf * 4 + 2 * cc], k.x, k.y);
+                        mma_e4m3(s[j], qa[hf * 4 + 2 * cc + 1], k.z, k.w);
+                    }
             next_unit();
             // ---- weights
             const float f = rf * ks;

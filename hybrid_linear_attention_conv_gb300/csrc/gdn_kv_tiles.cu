@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ tiles
-        const int page_rows = min(1 << p.log2_page, kN), boxes = kN / page_rows;
+        const int page_rows = 1 << p.log2_page;  // of a box: 32, 64 or 128
         int u = 0, g = 0, issued = 0;  // ring units (keys, values), tiles
         for (; w.settle(p); w.advance(p)) {
             // eight tiles' places and scales at a time: lane = 4 tile + 32-token stretch
@@ -337,15 +337,20 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                     if (*dead) continue;
                     issued = u + 1;
                     const uint32_t dst = tc::smem_u32(sm.ring[slot]);
-                    if (lane == 0) tc::mbar_arrive_expect_tx(full + 8 * slot, kSlot);
-                    for (int i = 0; i < boxes; ++i) {
-                        const int row = __shfl_sync(~0u, y, 4 * k + i * (4 / boxes));
-                        if (lane == 0)
+                    int row[4];
 #pragma unroll
-                            for (int hf = 0; hf < kHalves; ++hf)
-                                tc::tma_load_2d(dst + hf * kHalfBytes + i * page_rows * 128, kv ? &p.tm_v : &p.tm_k, hf * 128, row,
-                                                full + 8 * slot);
+                    for (int i = 0; i < 4; ++i) row[i] = __shfl_sync(~0u, y, 4 * k + i);
+                    const void* map = kv ? &p.tm_v : &p.tm_k;
+                    if (tc::elect_one()) {  // (a copy's operands are uniform registers: not under a test of the lane number)
+                        tc::mbar_arrive_expect_tx(full + 8 * slot, kSlot);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if ((i * 32) % page_rows == 0)
+#pragma unroll
+                                for (int hf = 0; hf < kHalves; ++hf)
+                                    tc::tma_load_2d(dst + hf * kHalfBytes + i * 32 * 128, map, hf * 128, row[i], full + 8 * slot);
                     }
+                    __syncwarp();
                 }
             }
         }
