@@ -11,28 +11,30 @@
 //
 // Bound by the cache's bytes: 2 d bytes a token and key/value head, against
 // 4 d flops for each of at most eight rows.  Both products run on
-// mma.sync.m16n8k32 with e4m3 operands, so no code is ever converted: the
-// eight rows' q, and their weights, are split into two e4m3 numbers (hi + lo),
-// hi in rows 0..7 of the tile and lo in rows 8..15, which this many rows would
-// leave empty.  An accumulator's two halves then lie in one thread.
-// tcgen05's tiles of 128 rows would be fifteen sixteenths empty here.
+// mma.sync.m16n8k16 with the codes, converted exactly to f16, as the 16-row
+// operand, and the eight rows as the n = 8 one, so no part of a tile is empty:
+//   S^T [tokens x rows] = K Q^T,     O^T [columns x rows] += V^T P^T.
+// q (bf16, times a power of two) is exact in f16, a weight is rounded by 2^-11.
+// (mma.sync on e4m3 operands is no shorter way: it took 870 instructions for a tile of
+// 32 tokens x 128, with q and the weights as two e4m3 numbers each.  tcgen05's
+// tiles of 128 rows would be fifteen sixteenths empty here.)
 //
 // Layout.  A contraction's index may be permuted as long as both operands
-// agree, and so may an output's columns, so both operands of both products
-// come straight from 16-byte shared-memory reads and from the thread's own
-// accumulators.  Lane = 4 g + q4:
-//   keys    token 8 j + g of a 32-token tile, its bytes 32 q4 .. 32 q4 + 31 of
+// agree, and so may an output's rows, so everything comes straight from 16-byte
+// shared-memory reads and from the thread's own accumulators.  Lane = 4 g + q4:
+//   keys    tokens 8 j + g of a 32-token tile, bytes 32 q4 .. 32 q4 + 31 of
 //           each 128: chunks 2 q4 and 2 q4 + 1 (c ^ (token & 7) after the swizzle:
 //           a quarter-warp's eight chunks fall into eight bank groups);
-//   logits  row g, tokens 8 j + 2 q4 and + 1;
-//   values  for the same eight tokens, chunk g of each 128 columns, transposed
-//           4 x 4 bytes at a time; column tile e then holds columns 16 g + e;
-//   output  row g, columns 32 q4 + e and 32 q4 + 16 + e: 32 in a row.
+//   logits  tokens g and g + 8 of each 16, rows 2 q4 and 2 q4 + 1; the weights of eight
+//           tokens become the second product's operand by one 8 x 8 transpose;
+//   values  tokens 2 q4, 2 q4 + 1 of each eight, chunk g of each 128 columns; bytes of
+//           two tokens are paired by a permute before they are converted;
+//   output  rows 2 q4 and 2 q4 + 1, columns 16 g .. 16 g + 15 of each 128.
 //
 // A warp is a worker of its own: it has a ring of tiles that it fills with TMA
 // loads and its own m, sum and output, and takes every fourth 32-token tile of
 // the CTA's part; nothing synchronises the CTA inside a part.  The list of all
-// (request, head, row block, tile) is cut evenly over the CTAs, two to an SM;
+// (request, head, row block, tile) is cut evenly over the CTAs, two or three to an SM;
 // a (request, head, row block) that spans several CTAs is joined by the last
 // of them to finish, in CTA order, so results do not depend on timing.
 #include <algorithm>
@@ -49,7 +51,10 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 32;               // tokens
 constexpr int kRows = 8;
-constexpr int kRingBytes = 24 * 1024;   // a warp's ring: 3 units of 8 KB or 6 of 4 KB
+// CTAs of an SM, and a warp's ring (3 units of 8 KB, or 4 of 4 KB): with 256
+// columns a thread needs more than the 168 registers that twelve warps leave it.
+__host__ __device__ constexpr int per_sm(int d) { return d == 256 ? 2 : 3; }
+__host__ __device__ constexpr int ring_bytes(int d) { return d == 256 ? 24 * 1024 : 16 * 1024; }
 constexpr float kPScale = 8.0f;         // weights are held times 2^8: e4m3 reaches 448
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr int kItemCost = 8;            // an item's beginning and end, in tiles
@@ -57,10 +62,10 @@ constexpr int kMinTiles = 16;           // what a CTA takes at least
 
 template <int D>
 struct RowsSmem {
-    alignas(1024) uint8_t ring[kWarps][kRingBytes];
+    alignas(1024) uint8_t ring[kWarps][ring_bytes(D)];
     alignas(16) float merge[kRows * D];     // one warp's output on its way to another
     float ml[kWarps][2][kRows];
-    alignas(8) uint64_t full[kWarps][6];
+    alignas(8) uint64_t full[kWarps][4];
     long long scan[kWarps];
     long long at_rest;                      // the CTA's first tile inside request at_b
     int at_b;
@@ -90,40 +95,27 @@ __device__ __forceinline__ Request request(const KvAttnParams& p, int b) {
     return r;
 }
 
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Bytes of four tokens (words r0..r3, four columns each) to four columns of
-// four tokens each.
-__device__ __forceinline__ void transpose4(uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3, uint32_t (&w)[4]) {
-    const uint32_t x0 = __byte_perm(r0, r1, 0x5140), x1 = __byte_perm(r0, r1, 0x7362);
-    const uint32_t y0 = __byte_perm(r2, r3, 0x5140), y1 = __byte_perm(r2, r3, 0x7362);
-    w[0] = __byte_perm(x0, y0, 0x5410);
-    w[1] = __byte_perm(x0, y0, 0x7632);
-    w[2] = __byte_perm(x1, y1, 0x5410);
-    w[3] = __byte_perm(x1, y1, 0x7632);
+// Transpose of an 8 x 8 matrix of f16: lane 4 g + q holds elements 2 q, 2 q + 1 of row g.
+__device__ __forceinline__ uint32_t transpose8(uint32_t w) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
+    return r;
 }
 
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// Running softmax state of one row (row g, the same in its four lanes but for
-// l and the output columns, which are the lane's own).
-template <int D>
-struct RowState {
-    float m, l;
-    float o[D / 8][2];  // [half * 16 + e]: columns half * 128 + 32 q4 + e and + 16 + e
-};
-
 __device__ __forceinline__ float factor(float m, float top) { return m == top ? 1.0f : ex2(m - top); }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) gdn_kv_attn_rows_kernel(const __grid_constant__ KvAttnParams p) {
+__global__ void __launch_bounds__(kThreads, per_sm(D)) gdn_kv_attn_rows_kernel(const __grid_constant__ KvAttnParams p) {
     constexpr int kUnit = kTile * D;                 // a tile's keys or values
-    constexpr int kUnits = kRingBytes / kUnit;
+    constexpr int kUnits = ring_bytes(D) / kUnit;
     constexpr int kHalves = D / 128;
     extern __shared__ uint8_t smem_raw[];
     RowsSmem<D>& sm = *reinterpret_cast<RowsSmem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -239,28 +231,37 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_kv_attn_rows_kernel(const __g
     if (more) begin();
     while (more) {
         // rows of this block: row -> query i, head of the group
-        const int block = item / p.Hkv, row = block * kRows + g;
-        const bool have = row < r.n * p.G;
-        const int qi = have ? row / p.G : 0, head = h * p.G + (have ? row - qi * p.G : 0);
-        const int base = r.L - r.n;                     // tokens that every query sees
-        const int seen = have ? base + qi + 1 : 0;      // causal: tokens below this
-        const unsigned long long tree = p.tree != nullptr && have ? (unsigned long long)p.tree[r.row0 + qi] : 0ull;
+        const int block = item / p.Hkv, base = r.L - r.n;  // base: tokens that every query sees
+        auto find = [&](int local, int& qi, int64_t& at) {  // at: of the row's output; false: no such row
+            const int row = block * kRows + local;
+            const bool have = row < r.n * p.G;
+            qi = have ? row / p.G : 0;
+            at = have ? (int64_t)(r.row0 + qi) * p.Hq + h * p.G + row - qi * p.G : 0;
+            return have;
+        };
+        int qi[2];
+        int64_t at[2];
+        const bool have[2] = {find(2 * q4, qi[0], at[0]), find(2 * q4 + 1, qi[1], at[1])};
+        const int seen[2] = {have[0] ? base + qi[0] + 1 : 0, have[1] ? base + qi[1] + 1 : 0};  // causal: tokens below this
         const int all_see = max(0, min(r.L, p.tree != nullptr ? base : base + (block * kRows) / p.G + 1));
         ksC = ksI;
         vsC = vsI;
 
-        // q as hi + lo, times a power of two that brings its largest to (224, 448]
-        uint32_t qa[kHalves * 4][4];
-        float rf;
+        // q (row g), times a power of two that brings its largest to (224, 448], in f16
+        uint32_t qb[kHalves * 8][2];
+        float rf[2];  // of rows 2 q4 and 2 q4 + 1
         {
-            const uint16_t* src = p.q + (int64_t)(r.row0 + qi) * p.ldq + (int64_t)head * D + 32 * q4;
+            int qig;
+            int64_t atg;
+            const bool haveg = find(g, qig, atg);
+            const uint16_t* src = p.q + (int64_t)(r.row0 + qig) * p.ldq + (atg - (int64_t)(r.row0 + qig) * p.Hq) * D + 32 * q4;
             uint4 w[kHalves][4];
             uint32_t m2 = 0;
 #pragma unroll
             for (int hf = 0; hf < kHalves; ++hf)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    w[hf][c] = have ? *reinterpret_cast<const uint4*>(src + hf * 128 + c * 8) : make_uint4(0, 0, 0, 0);
+                    w[hf][c] = haveg ? *reinterpret_cast<const uint4*>(src + hf * 128 + c * 8) : make_uint4(0, 0, 0, 0);
                     m2 = __vmaxu2(m2, w[hf][c].x & 0x7fff7fffu);
                     m2 = __vmaxu2(m2, w[hf][c].y & 0x7fff7fffu);
                     m2 = __vmaxu2(m2, w[hf][c].z & 0x7fff7fffu);
@@ -273,27 +274,24 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_kv_attn_rows_kernel(const __g
             const int e = finite ? scale_exp_of_bf16(top) : 0;
             const float inv = exp2_int(-e);
             // a query that is not finite makes its row NaN, through the row's factor
-            rf = finite ? exp2_int(e) * p.scale_log2 : __int_as_float(0x7fffffff);
+            const float mine = finite ? exp2_int(e) * p.scale_log2 : __int_as_float(0x7fffffff);
+            rf[0] = __shfl_sync(~0u, mine, 8 * q4);
+            rf[1] = __shfl_sync(~0u, mine, 8 * q4 + 4);
 #pragma unroll
             for (int hf = 0; hf < kHalves; ++hf)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint32_t u[4] = {w[hf][c].x, w[hf][c].y, w[hf][c].z, w[hf][c].w};
-                    float f[8];
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        f[2 * k] = finite ? __uint_as_float(u[k] << 16) * inv : 0.0f;
-                        f[2 * k + 1] = finite ? __uint_as_float(u[k] & 0xffff0000u) * inv : 0.0f;
+                        const uint32_t u = finite ? word_of(w[hf][c], k) : 0u;
+                        qb[hf * 8 + 2 * c + (k >> 1)][k & 1] = f16x2(__uint_as_float(u << 16) * inv, __uint_as_float(u & 0xffff0000u) * inv);
                     }
-                    split4_f16(f[0], f[1], f[2], f[3], qa[hf * 4 + c][0], qa[hf * 4 + c][1]);
-                    split4_f16(f[4], f[5], f[6], f[7], qa[hf * 4 + c][2], qa[hf * 4 + c][3]);
-                }
         }
 
-        float m = -INFINITY, l = 0.0f;
-        float o[kHalves * 16][4];
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+        float o[kHalves * 8][4];
 #pragma unroll
-        for (int e = 0; e < kHalves * 16; ++e) o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.0f;
+        for (int e = 0; e < kHalves * 8; ++e) o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.0f;
 
         auto wait_unit = [&]() {
             if (!tc::mbar_wait(bars + 8 * slot, parity, p.wait_ns)) {
@@ -317,102 +315,129 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_kv_attn_rows_kernel(const __g
                 vsC = vsI;
             }
             const float ks = __shfl_sync(~0u, ksC, i & 31), vs = __shfl_sync(~0u, vsC, i & 31), lv = __log2f(vs);
-            // ---- logits
+            // ---- logits: s[mt] of tokens 16 mt + g (0, 1) and 16 mt + 8 + g (2, 3), rows 2 q4 and 2 q4 + 1
             wait_unit();
-            float s[4][4];
+            float s[2][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
+            for (int mt = 0; mt < 2; ++mt) s[mt][0] = s[mt][1] = s[mt][2] = s[mt][3] = 0.0f;
 #pragma unroll
             for (int hf = 0; hf < kHalves; ++hf)
 #pragma unroll
-                for (int cc = 0; cc < 2; ++cc)
+                for (int cc = 0; cc < 2; ++cc) {
+                    uint4 k[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {  // four accumulators in turn: an MMA's result is 22 cycles away
-                        const uint4 k = *reinterpret_cast<const uint4*>(ring + slot * kUnit + hf * (kTile * 128) + (8 * j + g) * 128 + (((2 * q4 + cc) ^ g) << 4));
-                        mma_e4m3(s[j], qa[hf * 4 + 2 * cc], k.x, k.y);
-                        mma_e4m3(s[j], qa[hf * 4 + 2 * cc + 1], k.z, k.w);
-                    }
+                    for (int j = 0; j < 4; ++j)
+                        k[j] = *reinterpret_cast<const uint4*>(ring + slot * kUnit + hf * (kTile * 128) + (8 * j + g) * 128 + (((2 * q4 + cc) ^ g) << 4));
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int mt = 0; mt < 2; ++mt) {
+                            const uint32_t w0 = word_of(k[2 * mt], c), w1 = word_of(k[2 * mt + 1], c);
+                            const uint32_t(&b)[2] = qb[hf * 8 + cc * 4 + c];
+                            mma_f16(s[mt], f16x2_of_e4m3x2(w0), f16x2_of_e4m3x2(w1), f16x2_of_e4m3x2(w0 >> 16), f16x2_of_e4m3x2(w1 >> 16), b[0], b[1]);
+                        }
+                }
             next_unit();
             // ---- weights
-            const float f = rf * ks;
-            float t[8];
+            float t[4][2];  // tokens 8 j + g
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                t[2 * j] = fmaf(s[j][0] + s[j][2], f, lv);
-                t[2 * j + 1] = fmaf(s[j][1] + s[j][3], f, lv);
-            }
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) t[j][z] = fmaf(s[j >> 1][2 * (j & 1) + z], rf[z] * ks, lv);
             if (pos0 + kTile > all_see) {  // some row does not see some token
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int pos = pos0 + 8 * (k >> 1) + 2 * q4 + (k & 1);
-                    const int node = pos - base;
-                    const bool vis = p.tree != nullptr ? have && pos < r.L && (node < 0 || (node < 64 && ((tree >> (node & 63)) & 1)))
-                                                       : pos < seen;
-                    t[k] = vis ? t[k] : -INFINITY;
+                for (int z = 0; z < 2; ++z) {
+                    const unsigned long long tree = p.tree != nullptr && have[z] ? (unsigned long long)p.tree[r.row0 + qi[z]] : 0ull;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int pos = pos0 + 8 * j + g, node = pos - base;
+                        const bool vis = p.tree != nullptr ? have[z] && pos < r.L && (node < 0 || (node < 64 && ((tree >> (node & 63)) & 1)))
+                                                           : pos < seen[z];
+                        t[j][z] = vis ? t[j][z] : -INFINITY;
+                    }
                 }
             }
-            float top = t[0];
+            float top[2];
 #pragma unroll
-            for (int k = 1; k < 8; ++k) top = fmaxf(top, t[k]);
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-            const float m_new = fmaxf(m, top);
-            if (__any_sync(~0u, m_new > m)) {
-                const float c = factor(m, m_new);
-                l *= c;
+            for (int z = 0; z < 2; ++z) {
+                top[z] = fmaxf(fmaxf(t[0][z], t[1][z]), fmaxf(t[2][z], t[3][z]));
+                top[z] = fmaxf(top[z], __shfl_xor_sync(~0u, top[z], 4));
+                top[z] = fmaxf(top[z], __shfl_xor_sync(~0u, top[z], 8));
+                top[z] = fmaxf(top[z], __shfl_xor_sync(~0u, top[z], 16));
+                top[z] = fmaxf(top[z], m[z]);
+            }
+            if (__any_sync(~0u, top[0] > m[0] || top[1] > m[1])) {
+                const float c0 = factor(m[0], top[0]), c1 = factor(m[1], top[1]);
+                l[0] *= c0;
+                l[1] *= c1;
 #pragma unroll
-                for (int e = 0; e < kHalves * 16; ++e) {
-                    o[e][0] *= c;
-                    o[e][1] *= c;
-                    o[e][2] *= c;
-                    o[e][3] *= c;
+                for (int e = 0; e < kHalves * 8; ++e) {
+                    o[e][0] *= c0;
+                    o[e][1] *= c1;
+                    o[e][2] *= c0;
+                    o[e][3] *= c1;
                 }
-                m = m_new;
+                m[0] = top[0];
+                m[1] = top[1];
             }
-            const float shift = kPScale - (m == -INFINITY ? 0.0f : m);
-            float w[8], sum = 0.0f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                w[k] = ex2(t[k] + shift);  // a token that is not seen: 2^-inf = 0
-                sum += w[k];
-            }
-            if (sum != 0.0f) l = fmaf(sum, __fdividef(1.0f, vs), l);  // a row that sees nothing here takes nothing from the block's scale
-            uint32_t pa[4];
+            uint32_t pb[4];
             {
-                split4_f16(w[0], w[1], w[2], w[3], pa[0], pa[1]);
-                split4_f16(w[4], w[5], w[6], w[7], pa[2], pa[3]);
+                const float a0 = kPScale - (m[0] == -INFINITY ? 0.0f : m[0]), a1 = kPScale - (m[1] == -INFINITY ? 0.0f : m[1]);
+                float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float e0 = ex2(t[j][0] + a0), e1 = ex2(t[j][1] + a1);  // a token that is not seen: 2^-inf = 0
+                    sum[0] += e0;
+                    sum[1] += e1;
+                    pb[j] = transpose8(f16x2(e0, e1));
+                }
+                // a row that sees nothing here takes nothing from the block's scale
+                const float iv = __fdividef(1.0f, vs);
+                if (sum[0] != 0.0f) l[0] = fmaf(sum[0], iv, l[0]);
+                if (sum[1] != 0.0f) l[1] = fmaf(sum[1], iv, l[1]);
             }
-            // ---- output
+            // ---- output: column tile e holds columns 16 g + 2 e (0, 1) and 16 g + 2 e + 1 (2, 3)
             wait_unit();
             const bool tail = pos0 + kTile > r.L;
 #pragma unroll
             for (int hf = 0; hf < kHalves; ++hf) {
                 uint4 v[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int tok = 8 * (k >> 1) + 2 * q4 + (k & 1);
-                    v[k] = *reinterpret_cast<const uint4*>(ring + slot * kUnit + hf * (kTile * 128) + tok * 128 + ((g ^ (tok & 7)) << 4));
-                    if (tail && pos0 + tok >= r.L) v[k] = make_uint4(0, 0, 0, 0);  // whatever lies past the end
+                for (int k = 0; k < 8; ++k)
+                    v[k] = *reinterpret_cast<const uint4*>(ring + slot * kUnit + hf * (kTile * 128) + (8 * (k >> 1) + 2 * q4 + (k & 1)) * 128 +
+                                                           ((g ^ ((2 * q4 + (k & 1)) & 7)) << 4));
+                if (tail) {  // whatever lies past the end: zeros
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (pos0 + 8 * (k >> 1) + 2 * q4 + (k & 1) >= r.L) v[k] = make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t b0[4], b1[4];
-                    transpose4(word_of(v[0], c), word_of(v[1], c), word_of(v[2], c), word_of(v[3], c), b0);
-                    transpose4(word_of(v[4], c), word_of(v[5], c), word_of(v[6], c), word_of(v[7], c), b1);
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) mma_e4m3(o[hf * 16 + 4 * c + k], pa, b0[k], b1[k]);
-                }
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t sel = half ? 0x7362 : 0x5140;  // bytes 2 half, 2 half + 1 of two tokens, paired
+                        uint32_t x[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) x[k] = __byte_perm(word_of(v[2 * k], c), word_of(v[2 * k + 1], c), sel);
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+                            mma_f16(o[hf * 8 + 2 * c + half], f16x2_of_e4m3x2(x[2 * u]), f16x2_of_e4m3x2(x[2 * u] >> 16), f16x2_of_e4m3x2(x[2 * u + 1]),
+                                    f16x2_of_e4m3x2(x[2 * u + 1] >> 16), pb[2 * u], pb[2 * u + 1]);
+                    }
             }
             next_unit();
         }
-        l += __shfl_xor_sync(~0u, l, 1);
-        l += __shfl_xor_sync(~0u, l, 2);
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            l[z] += __shfl_xor_sync(~0u, l[z], 4);
+            l[z] += __shfl_xor_sync(~0u, l[z], 8);
+            l[z] += __shfl_xor_sync(~0u, l[z], 16);
+        }
 
         // ---- the next stretch's copies go out before this one's output is put together
         const long long tile0 = x - v0 + kItemCost;  // the place of the item's first tile
         const int c0 = (int)(tile0 / W), c1 = (int)((tile0 + r.tiles - 1) / W);
         const bool from_start = t0 == 0;
-        const int64_t at = (int64_t)(r.row0 + qi) * p.Hq + head;
         x += t1 + kItemCost - v0;
         v0 = 0;
         ++item;
@@ -420,40 +445,37 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_kv_attn_rows_kernel(const __g
         if (more) begin();
 
         // ---- the four warps' states into warp 0's, one after another
-        float acc[kHalves * 16][2];
+        auto take = [&](float mo0, float mo1, float lo0, float lo1, const float* from) {  // from: this lane's values, 32 lanes apart by float4
+            const float top0 = fmaxf(m[0], mo0), top1 = fmaxf(m[1], mo1);
+            const float a0 = factor(m[0], top0), a1 = factor(m[1], top1), b0 = factor(mo0, top0), b1 = factor(mo1, top1);
+            l[0] = l[0] * a0 + lo0 * b0;
+            l[1] = l[1] * a1 + lo1 * b1;
+            m[0] = top0;
+            m[1] = top1;
 #pragma unroll
-        for (int e = 0; e < kHalves * 16; ++e) {
-            acc[e][0] = o[e][0] + o[e][2];
-            acc[e][1] = o[e][1] + o[e][3];
-        }
-        auto take = [&](float m_other, float l_other, const float* from) {  // from: this lane's values, 32 lanes apart by float4
-            const float top = fmaxf(m, m_other), fa = factor(m, top), fb = factor(m_other, top);
-            l = l * fa + l_other * fb;
-            m = top;
-#pragma unroll
-            for (int e = 0; e < kHalves * 16; e += 2) {
-                const float4 u = *reinterpret_cast<const float4*>(from + (e / 2) * 128 + lane * 4);
-                acc[e][0] = acc[e][0] * fa + u.x * fb;
-                acc[e][1] = acc[e][1] * fa + u.y * fb;
-                acc[e + 1][0] = acc[e + 1][0] * fa + u.z * fb;
-                acc[e + 1][1] = acc[e + 1][1] * fa + u.w * fb;
+            for (int e = 0; e < kHalves * 8; ++e) {
+                const float4 u = *reinterpret_cast<const float4*>(from + e * 128 + lane * 4);
+                o[e][0] = o[e][0] * a0 + u.x * b0;
+                o[e][1] = o[e][1] * a1 + u.y * b1;
+                o[e][2] = o[e][2] * a0 + u.z * b0;
+                o[e][3] = o[e][3] * a1 + u.w * b1;
             }
         };
         auto give = [&](float* to) {
 #pragma unroll
-            for (int e = 0; e < kHalves * 16; e += 2)
-                *reinterpret_cast<float4*>(to + (e / 2) * 128 + lane * 4) =
-                    make_float4(acc[e][0], acc[e][1], acc[e + 1][0], acc[e + 1][1]);
+            for (int e = 0; e < kHalves * 8; ++e) *reinterpret_cast<float4*>(to + e * 128 + lane * 4) = make_float4(o[e][0], o[e][1], o[e][2], o[e][3]);
         };
         auto merge_warps = [&]() {
-            if (q4 == 0) {
-                sm.ml[warp][0][g] = m;
-                sm.ml[warp][1][g] = l;
+            if (g == 0) {
+                sm.ml[warp][0][2 * q4] = m[0];
+                sm.ml[warp][0][2 * q4 + 1] = m[1];
+                sm.ml[warp][1][2 * q4] = l[0];
+                sm.ml[warp][1][2 * q4 + 1] = l[1];
             }
             for (int w = 1; w < kWarps; ++w) {
                 if (warp == w) give(sm.merge);
                 __syncthreads();
-                if (warp == 0) take(sm.ml[w][0][g], sm.ml[w][1][g], sm.merge);
+                if (warp == 0) take(sm.ml[w][0][2 * q4], sm.ml[w][0][2 * q4 + 1], sm.ml[w][1][2 * q4], sm.ml[w][1][2 * q4 + 1], sm.merge);
                 __syncthreads();
             }
         };
@@ -467,9 +489,9 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_kv_attn_rows_kernel(const __g
             float* part = p.partials + ((size_t)blockIdx.x * 2 + (from_start ? 1 : 0)) * kPart;
             if (warp == 0) {
                 give(part);
-                if (q4 == 0) {
-                    part[kRows * D + g] = m;
-                    part[kRows * D + kRows + g] = l;
+                if (g == 0) {
+                    *reinterpret_cast<float2*>(part + kRows * D + 2 * q4) = make_float2(m[0], m[1]);
+                    *reinterpret_cast<float2*>(part + kRows * D + kRows + 2 * q4) = make_float2(l[0], l[1]);
                 }
                 __threadfence();
                 __syncwarp();
@@ -485,37 +507,39 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_kv_attn_rows_kernel(const __g
             write = false;
             if (join) {  // uniform in the CTA
                 __threadfence();
-                m = -INFINITY;
-                l = 0.0f;
+                m[0] = m[1] = -INFINITY;
+                l[0] = l[1] = 0.0f;
 #pragma unroll
-                for (int e = 0; e < kHalves * 16; ++e) acc[e][0] = acc[e][1] = 0.0f;
+                for (int e = 0; e < kHalves * 8; ++e) o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.0f;
                 for (int c = c0 + warp; c <= c1; c += kWarps) {
                     const float* other = p.partials + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * kPart;
-                    take(__ldcg(other + kRows * D + g), __ldcg(other + kRows * D + kRows + g), other);
+                    const float2 mo = __ldcg(reinterpret_cast<const float2*>(other + kRows * D + 2 * q4));
+                    const float2 lo = __ldcg(reinterpret_cast<const float2*>(other + kRows * D + kRows + 2 * q4));
+                    take(mo.x, mo.y, lo.x, lo.y, other);
                 }
                 merge_warps();
                 write = warp == 0;
             }
         }
-        if (write && have) {
-            const bool empty = l == 0.0f;  // no token seen: zeros
-            const float inv = empty ? 0.0f : 1.0f / l;
+        if (write) {
 #pragma unroll
-            for (int hf = 0; hf < kHalves; ++hf) {
-                uint16_t* dst = p.out + at * D + hf * 128 + 32 * q4;
+            for (int z = 0; z < 2; ++z) {
+                if (!have[z]) continue;
+                const bool empty = l[z] == 0.0f;  // no token seen: zeros
+                const float inv = empty ? 0.0f : 1.0f / l[z];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {  // columns 8 c .. 8 c + 7
-                    uint32_t u[4];
+                for (int hf = 0; hf < kHalves; ++hf) {
+                    uint4* dst = reinterpret_cast<uint4*>(p.out + at[z] * D + hf * 128 + 16 * g);
+                    uint32_t u[8];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int e = (8 * c + 2 * k) & 15, z = c >> 1;
-                        u[k] = tc::pack_bf16(__float2bfloat16_rn(acc[hf * 16 + e][z] * inv), __float2bfloat16_rn(acc[hf * 16 + e + 1][z] * inv));
-                    }
-                    *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(u[0], u[1], u[2], u[3]);
+                    for (int e = 0; e < 8; ++e)
+                        u[e] = tc::pack_bf16(__float2bfloat16_rn(o[hf * 8 + e][z] * inv), __float2bfloat16_rn(o[hf * 8 + e][2 + z] * inv));
+                    dst[0] = make_uint4(u[0], u[1], u[2], u[3]);
+                    dst[1] = make_uint4(u[4], u[5], u[6], u[7]);
                 }
+                if (p.lse != nullptr && g == 0)
+                    p.lse[at[z]] = empty ? -INFINITY : ((m[z] == -INFINITY ? 0.0f : m[z]) - kPScale + log2f(l[z])) * 0.69314718055994531f;
             }
-            if (p.lse != nullptr && q4 == 0)
-                p.lse[at] = empty ? -INFINITY : ((m == -INFINITY ? 0.0f : m) - kPScale + log2f(l)) * 0.69314718055994531f;
         }
     }
 }
@@ -532,14 +556,14 @@ cudaError_t launch(KvAttnParams& p, cudaStream_t s) {
         err[dev] = cudaFuncSetAttribute(gdn_kv_attn_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (err[dev] != cudaSuccess) return err[dev];
-    const int grid = std::min(2 * device_sm_count(), kKvMaxCtas);
+    const int grid = std::min(per_sm(D) * device_sm_count(), kKvMaxCtas);
     gdn_kv_attn_rows_kernel<D><<<grid, kThreads, smem, s>>>(p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t kv_attn_rows_workspace(int d) { return (size_t)2 * std::min(2 * device_sm_count(), kKvMaxCtas) * (kRows * d + 2 * kRows) * 4; }
+size_t kv_attn_rows_workspace(int d) { return (size_t)2 * std::min(per_sm(d) * device_sm_count(), kKvMaxCtas) * (kRows * d + 2 * kRows) * 4; }
 
 cudaError_t launch_kv_attn_rows(KvAttnParams& p, int d, cudaStream_t s) { return d == 256 ? launch<256>(p, s) : launch<128>(p, s); }
 
