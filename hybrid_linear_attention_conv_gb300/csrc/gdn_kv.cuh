@@ -76,6 +76,8 @@ struct KvAttnParams {
     float* lse;                 // [T, Hq] or nullptr
     int* status;                // workspace: the status word,
     unsigned* counters;         // a counter for each CTA (zero between calls),
+    int* spans;                 // how many CTAs further the item goes that begins in a CTA,
+    int64_t* span_rows;         // its eight rows' places in out (-1: none),
     float* partials;            // and the partial results
     uint64_t wait_ns;
     int64_t ldq;
@@ -84,9 +86,11 @@ struct KvAttnParams {
     unsigned group_magic;       // ceil(2^22 / G)
 };
 
-// Workspace: 256 bytes of status, the counters, then the partial results.
+// Workspace: 256 bytes of status, the counters, spans and their rows, then the partial results.
 constexpr int kKvMaxCtas = 1024;
-constexpr size_t kKvPartialsAt = 256 + (size_t)kKvMaxCtas * 4;
+constexpr size_t kKvSpansAt = 256 + (size_t)kKvMaxCtas * 4;
+constexpr size_t kKvSpanRowsAt = kKvSpansAt + (size_t)kKvMaxCtas * 4;
+constexpr size_t kKvPartialsAt = kKvSpanRowsAt + (size_t)kKvMaxCtas * 8 * 8;
 
 cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t s);
 cudaError_t launch_kv_plan(const KvPlanParams& p, cudaStream_t s);

@@ -35,8 +35,11 @@
 // loads and its own m, sum and output, and takes every fourth 32-token tile of
 // the CTA's part; nothing synchronises the CTA inside a part.  The list of all
 // (request, head, row block, tile) is cut evenly over the CTAs, two or three to an SM;
-// a (request, head, row block) that spans several CTAs is joined by the last
-// of them to finish, in CTA order, so results do not depend on timing.
+// a (request, head, row block) that spans several CTAs leaves its parts in the
+// workspace, and a second kernel joins them, in CTA order, so results do not
+// depend on timing.  (Joined by the last CTA to finish, the 76 parts of an item
+// took 15 us and more: one SM's reads, a round after another, by code that the
+// stream of the cache had driven out of the L2.)
 #include <algorithm>
 #include <mutex>
 
@@ -55,7 +58,7 @@ constexpr int kRows = 8;
 // columns a thread needs more than the 168 registers that twelve warps leave it.
 __host__ __device__ constexpr int per_sm(int d) { return d == 256 ? 2 : 3; }
 __host__ __device__ constexpr int ring_bytes(int d) { return d == 256 ? 24 * 1024 : 16 * 1024; }
-constexpr float kPScale = 8.0f;         // weights are held times 2^8: e4m3 reaches 448
+constexpr float kPScale = 8.0f;         // weights are held times 2^8
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr int kItemCost = 8;            // an item's beginning and end, in tiles
 constexpr int kMinTiles = 16;           // what a CTA takes at least
@@ -69,7 +72,6 @@ struct RowsSmem {
     long long scan[kWarps];
     long long at_rest;                      // the CTA's first tile inside request at_b
     int at_b;
-    unsigned last;
 };
 
 // A request's part of the list of tiles.  An item (head, row block) takes
@@ -112,6 +114,13 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i ==
 
 __device__ __forceinline__ float factor(float m, float top) { return m == top ? 1.0f : ex2(m - top); }
 
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l == 0.0f ? -INFINITY : ((m == -INFINITY ? 0.0f : m) - kPScale + log2f(l)) * 0.69314718055994531f;
+}
+
+// A part: an item's rows [8][d] as summed up, their m, their l.
+__host__ __device__ constexpr int part_floats(int d) { return kRows * d + 2 * kRows; }
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, per_sm(D)) gdn_kv_attn_rows_kernel(const __grid_constant__ KvAttnParams p) {
     constexpr int kUnit = kTile * D;                 // a tile's keys or values
@@ -124,6 +133,13 @@ __global__ void __launch_bounds__(kThreads, per_sm(D)) gdn_kv_attn_rows_kernel(c
     const uint32_t ring_at = tc::smem_u32(ring), bars = tc::smem_u32(sm.full[warp]);
     if (lane == 0)
         for (int i = 0; i < kUnits; ++i) tc::mbar_init(bars + 8 * i, 1);
+    if (tid == 0) {
+        tc::prefetch_map(&p.tm_k);
+        tc::prefetch_map(&p.tm_v);
+    }
+    // A programmatic dependent launch: nothing above touches memory that an earlier kernel may write.
+    tc::grid_wait();
+    if (tid == 0) p.spans[blockIdx.x] = 0;
 
     // Where this CTA's part of the list of tiles begins: prefix sums of the
     // requests' work, a stretch of requests to a thread.
@@ -481,46 +497,28 @@ __global__ void __launch_bounds__(kThreads, per_sm(D)) gdn_kv_attn_rows_kernel(c
         };
         merge_warps();
 
-        // ---- the whole item here: write it; else leave a part, and the last
-        // CTA of the item joins them all
-        bool write = warp == 0;
-        constexpr int kPart = kRows * D + 2 * kRows;
-        if (c0 != c1) {
-            float* part = p.partials + ((size_t)blockIdx.x * 2 + (from_start ? 1 : 0)) * kPart;
-            if (warp == 0) {
-                give(part);
-                if (g == 0) {
-                    *reinterpret_cast<float2*>(part + kRows * D + 2 * q4) = make_float2(m[0], m[1]);
-                    *reinterpret_cast<float2*>(part + kRows * D + kRows + 2 * q4) = make_float2(l[0], l[1]);
-                }
-                __threadfence();
-                __syncwarp();
-                if (lane == 0) {
-                    const unsigned n = atomicAdd(p.counters + c0, 1u);
-                    sm.last = n == (unsigned)(c1 - c0);
-                    if (sm.last) p.counters[c0] = 0;  // as the next call finds it
-                }
-            }
-            __syncthreads();
-            const bool join = sm.last != 0;
-            __syncthreads();
-            write = false;
-            if (join) {  // uniform in the CTA
-                __threadfence();
-                m[0] = m[1] = -INFINITY;
-                l[0] = l[1] = 0.0f;
+        // ---- the whole item here: write it; else leave a part
+        if (warp == 0 && c0 != c1) {
+            float* left = p.partials + ((size_t)blockIdx.x * 2 + (from_start ? 1 : 0)) * part_floats(D);
 #pragma unroll
-                for (int e = 0; e < kHalves * 8; ++e) o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.0f;
-                for (int c = c0 + warp; c <= c1; c += kWarps) {
-                    const float* other = p.partials + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * kPart;
-                    const float2 mo = __ldcg(reinterpret_cast<const float2*>(other + kRows * D + 2 * q4));
-                    const float2 lo = __ldcg(reinterpret_cast<const float2*>(other + kRows * D + kRows + 2 * q4));
-                    take(mo.x, mo.y, lo.x, lo.y, other);
+            for (int z = 0; z < 2; ++z) {
+                const int local = 2 * q4 + z;
+#pragma unroll
+                for (int hf = 0; hf < kHalves; ++hf) {
+                    float4* dst = reinterpret_cast<float4*>(left + local * D + hf * 128 + 16 * g);
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2)
+                        dst[e / 2] = make_float4(o[hf * 8 + e][z], o[hf * 8 + e][2 + z], o[hf * 8 + e + 1][z], o[hf * 8 + e + 1][2 + z]);
                 }
-                merge_warps();
-                write = warp == 0;
+                if (g == 0) {
+                    left[kRows * D + local] = m[z];
+                    left[kRows * D + kRows + local] = l[z];
+                    if (from_start) p.span_rows[blockIdx.x * kRows + local] = have[z] ? at[z] : -1;
+                }
             }
+            if (tid == 0 && from_start) p.spans[blockIdx.x] = c1 - c0;
         }
+        const bool write = warp == 0 && c0 == c1;
         if (write) {
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
@@ -537,11 +535,77 @@ __global__ void __launch_bounds__(kThreads, per_sm(D)) gdn_kv_attn_rows_kernel(c
                     dst[0] = make_uint4(u[0], u[1], u[2], u[3]);
                     dst[1] = make_uint4(u[4], u[5], u[6], u[7]);
                 }
-                if (p.lse != nullptr && g == 0)
-                    p.lse[at[z]] = empty ? -INFINITY : ((m[z] == -INFINITY ? 0.0f : m[z]) - kPScale + log2f(l[z])) * 0.69314718055994531f;
+                if (p.lse != nullptr && g == 0) p.lse[at[z]] = lse_of(m[z], l[z]);
             }
         }
     }
+}
+
+// Joins the parts of the item that begins in CTA blockIdx.y and goes on in later
+// ones.  A block has 512 consecutive values of the item's eight rows, a lane four times four
+// of them; each of its warps adds up every eighth part.
+constexpr int kJoinWarps = 8;
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) gdn_kv_join_rows_kernel(const int* spans, const int64_t* span_rows, const float* partials,
+                                                                           uint16_t* out, float* lse) {
+    __shared__ float4 acc[kJoinWarps][4][32];
+    __shared__ float ml[kJoinWarps][4][2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.y;
+    tc::grid_wait();
+    const int more = spans[c0];
+    if (more == 0) return;
+    auto part_of = [&](int c) { return partials + ((size_t)(c0 + c) * 2 + (c == 0 ? 1 : 0)) * part_floats(D); };
+    const int at0 = blockIdx.x * 128 + lane;  // by float4
+    float m[4], l[4];
+    float4 sum[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        m[k] = -INFINITY;
+        l[k] = 0.0f;
+        sum[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+#pragma unroll 1
+    for (int c = warp; c <= more; c += kJoinWarps) {
+        const float* part = part_of(c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int row = (blockIdx.x * 128 + k * 32) / (D / 4);
+            const float mo = part[kRows * D + row], lo = part[kRows * D + kRows + row];
+            const float4 u = reinterpret_cast<const float4*>(part)[at0 + k * 32];
+            const float top = fmaxf(m[k], mo), a = factor(m[k], top), b = factor(mo, top);
+            m[k] = top;
+            l[k] = l[k] * a + lo * b;
+            sum[k] = make_float4(sum[k].x * a + u.x * b, sum[k].y * a + u.y * b, sum[k].z * a + u.z * b, sum[k].w * a + u.w * b);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        acc[warp][k][lane] = sum[k];
+        if (lane == 0) {
+            ml[warp][k][0] = m[k];
+            ml[warp][k][1] = l[k];
+        }
+    }
+    __syncthreads();
+    if (warp >= 4) return;
+    // warp k: the k-th of the block's four stretches of 128 values
+    const int k = warp, i4 = at0 + k * 32, row = i4 / (D / 4);
+    float top = -INFINITY, total = 0.0f;
+    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, ml[w][k][0]);
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int w = 0; w < kJoinWarps; ++w) {
+        const float f = factor(ml[w][k][0], top);
+        const float4 u = acc[w][k][lane];
+        total = fmaf(ml[w][k][1], f, total);
+        v = make_float4(fmaf(u.x, f, v.x), fmaf(u.y, f, v.y), fmaf(u.z, f, v.z), fmaf(u.w, f, v.w));
+    }
+    const int64_t to = span_rows[c0 * kRows + row];
+    if (to < 0) return;
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    const int col = i4 % (D / 4) * 4;
+    *reinterpret_cast<uint2*>(out + to * D + col) = make_uint2(tc::pack_bf16(__float2bfloat16_rn(v.x * inv), __float2bfloat16_rn(v.y * inv)),
+                                                              tc::pack_bf16(__float2bfloat16_rn(v.z * inv), __float2bfloat16_rn(v.w * inv)));
+    if (lse != nullptr && col == 0) lse[to] = lse_of(top, total);
 }
 
 template <int D>
@@ -557,13 +621,27 @@ cudaError_t launch(KvAttnParams& p, cudaStream_t s) {
     });
     if (err[dev] != cudaSuccess) return err[dev];
     const int grid = std::min(per_sm(D) * device_sm_count(), kKvMaxCtas);
-    gdn_kv_attn_rows_kernel<D><<<grid, kThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, gdn_kv_attn_rows_kernel<D>, p);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(kRows * D / 512, (unsigned)grid);
+    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, gdn_kv_join_rows_kernel<D>, (const int*)p.spans, (const int64_t*)p.span_rows, (const float*)p.partials, p.out, p.lse);
 }
 
 }  // namespace
 
-size_t kv_attn_rows_workspace(int d) { return (size_t)2 * std::min(per_sm(d) * device_sm_count(), kKvMaxCtas) * (kRows * d + 2 * kRows) * 4; }
+size_t kv_attn_rows_workspace(int d) { return (size_t)2 * std::min(per_sm(d) * device_sm_count(), kKvMaxCtas) * part_floats(d) * 4; }
 
 cudaError_t launch_kv_attn_rows(KvAttnParams& p, int d, cudaStream_t s) { return d == 256 ? launch<256>(p, s) : launch<128>(p, s); }
 

@@ -111,6 +111,13 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
+// A tensor map on its way to the copy engine's cache.
+__device__ __forceinline__ void prefetch_map(const void* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+// Wait for the kernels before this one on the stream (a programmatic dependent launch).
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Barrier `id` among `threads` threads of the CTA.
 __device__ __forceinline__ void named_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
