@@ -207,6 +207,11 @@ __device__ __forceinline__ void append_run(const KvAppendParams& p, int t, int n
     const uint16_t* src = (is_v ? p.v : p.k) + (int64_t)head * p.d;
     const int64_t ld = is_v ? p.ldv : p.ldk;
     const int per_row = p.d >> 3, chunks = n * per_row, shift = p.d == 256 ? 5 : 4;
+    const int64_t page = slot >> p.log2_page;
+    const int at = (int)(slot & ((1 << p.log2_page) - 1));
+    float* scale = (is_v ? p.v_scale : p.k_scale) + page * p.Hkv + head;
+    uint8_t* block = (is_v ? p.v_cache : p.k_cache) + ((page * p.Hkv + head) << p.log2_page) * p.d;
+    const float old = at > 0 ? *scale : 0.0f;  // read before the maximum's barrier, replaced after it
     uint4 x[CH];
     uint32_t m2 = 0, missing = 0;
 #pragma unroll
@@ -229,13 +234,7 @@ __device__ __forceinline__ void append_run(const KvAppendParams& p, int t, int n
         for (int i = 0; i < CH; ++i) f = max_finite8(f, x[i]);
         top = reduce_max(f);
     }
-    const int64_t page = slot >> p.log2_page;
-    const int at = (int)(slot & ((1 << p.log2_page) - 1));
-    float* scale = (is_v ? p.v_scale : p.k_scale) + page * p.Hkv + head;
-    uint8_t* block = (is_v ? p.v_cache : p.k_cache) + ((page * p.Hkv + head) << p.log2_page) * p.d;
     const float fresh = exp2_int(scale_exp_of_bf16(top));
-    const float old = at > 0 ? *scale : 0.0f;
-    reduce_max(0u);  // every thread has read the old scale before it is replaced
     const bool poisoned = at > 0 && !(old > 0.0f && old < INFINITY);  // earlier rows that are not numbers stay so
     const float now = poisoned ? fresh : fmaxf(old, fresh);
     // the scales that this kernel writes are powers of two; one that is not
@@ -258,7 +257,7 @@ __device__ __forceinline__ void append_run(const KvAppendParams& p, int t, int n
 }
 
 template <int CH>
-__global__ void __launch_bounds__(kAppendThreads) gdn_kv_append_kernel(KvAppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, CH > 8 ? 2 : 4) gdn_kv_append_kernel(KvAppendParams p) {
     __shared__ uint32_t warp_max[2][kAppendWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int head = blockIdx.y, t0 = blockIdx.x * p.tile, P = 1 << p.log2_page;
@@ -266,42 +265,53 @@ __global__ void __launch_bounds__(kAppendThreads) gdn_kv_append_kernel(KvAppendP
     const int64_t last_slot = (int64_t)p.pages << p.log2_page;
 
     // Rows t0 .. t0 + tile - 1: a row begins a run unless it follows the row
-    // before it inside a page.  Every warp finds the same runs.
-    const int t = t0 + lane;
-    const bool mine = lane < p.tile && t < p.T;
-    const int64_t slot = mine ? p.slots[t] : -1;
-    const int64_t before = mine && t > 0 ? p.slots[t - 1] : -2;
-    const bool valid = slot >= 0 && slot < last_slot;
-    const bool begins = valid && (before != slot - 1 || (slot & (P - 1)) == 0);
-    uint32_t left = __ballot_sync(~0u, begins);
-    const uint32_t ends = ~__ballot_sync(~0u, valid && !begins);  // rows that do not continue a run
+    // before it inside a page.  A run ends within P rows of its first, so the
+    // slots of tile + P rows, read at once, a word of 32 to a warp, tell all.
+    __shared__ uint32_t goes_on[kAppendWarps], begins[kAppendWarps];  // bit l of word k: row t0 + 32 k + l
+    {
+        const int t = t0 + tid;
+        const int64_t slot = t < p.T && tid < p.tile + P ? p.slots[t] : -1;
+        int64_t prev = __shfl_up_sync(~0u, slot, 1);
+        if (lane == 0) prev = t > 0 && t < p.T ? p.slots[t - 1] : -2;
+        const bool valid = slot >= 0 && slot < last_slot;
+        const bool follows = valid && prev == slot - 1 && (slot & (P - 1)) != 0;
+        const uint32_t goes = __ballot_sync(~0u, follows), first = __ballot_sync(~0u, valid && !follows && tid < p.tile);
+        if (lane == 0) {
+            goes_on[warp] = goes;
+            begins[warp] = first;
+        }
+    }
+    __syncthreads();
     int phase = 0, nth = 0;
-    while (left) {  // uniform in the CTA
+    uint32_t left = begins[0];
+    for (int word = 0;;) {  // uniform in the CTA
+        if (left == 0) {
+            if (32 * ++word >= p.tile) break;
+            left = begins[word];
+            continue;
+        }
         const int l = __ffs(left) - 1;
         left &= left - 1;
-        const int64_t s0 = __shfl_sync(~0u, slot, l);
-        const int room = P - (int)(s0 & (P - 1));
-        const uint32_t after = l == 31 ? 0u : ends >> (l + 1);
-        int n = after ? __ffs(after) : 32 - l;  // a row past the tile does not continue in it
-        if (l + n >= p.tile) {  // up to the tile's end: the run may go on past it
-            n = p.tile - l;
-            while (n < room) {
-                const int u = t0 + l + n + lane;
-                const uint32_t stop = ~__ballot_sync(~0u, u < p.T && n + lane < room && p.slots[min(u, p.T - 1)] == s0 + n + lane);
-                if (stop) {
-                    n += __ffs(stop) - 1;
-                    break;
-                }
-                n += 32;
+        int n = 1, k = word, from = l + 1;  // rows that go on from the next one
+        while (true) {
+            if (from == 32) {
+                from = 0;
+                if (++k == kAppendWarps) break;
             }
+            const uint32_t ends = ~goes_on[k] >> from;
+            const int run = ends ? min(__ffs(ends) - 1, 32 - from) : 32 - from;
+            n += run;
+            if (run < 32 - from) break;
+            from = 32;
         }
-        n = min(n, min(room, p.T - (t0 + l)));
+        const int t_run = t0 + 32 * word + l;
+        const int64_t s0 = p.slots[t_run];
         if (n <= kAppendShort) {
             if (nth++ % kAppendWarps == warp)
-                append_run<kAppendShort>(p, t0 + l, n, s0, head, is_v, lane, 32,
+                append_run<kAppendShort>(p, t_run, n, s0, head, is_v, lane, 32,
                                          [](uint32_t m) { return __reduce_max_sync(~0u, m); });
         } else {
-            append_run<CH>(p, t0 + l, n, s0, head, is_v, tid, kAppendThreads, [&](uint32_t m) {
+            append_run<CH>(p, t_run, n, s0, head, is_v, tid, kAppendThreads, [&](uint32_t m) {
                 m = __reduce_max_sync(~0u, m);
                 if (lane == 0) warp_max[phase][warp] = m;
                 __syncthreads();
@@ -344,10 +354,9 @@ int check_row_stride(int64_t ld, int64_t row, const char* name) {
     return GDN_OK;
 }
 
-// Rows a CTA looks at.  Few rows are mostly single tokens, a warp each; among
-// many rows most belong to long runs, and a CTA that finds none has only cost
-// its launch.
-int append_tile_rows(int T) { return T <= 1024 ? kAppendWarps : 32; }
+// Rows a CTA looks at.  Few rows are mostly single tokens, a warp each; of many
+// rows most belong to long runs, of which about one begins in every P rows.
+int append_tile_rows(int T, int P) { return T <= 1024 ? kAppendWarps : P; }
 
 // cuTensorMapEncodeTiled from the driver, looked up once.
 PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
@@ -401,7 +410,7 @@ cudaError_t launch_kv_plan(const KvPlanParams& p, cudaStream_t s) {
 
 cudaError_t launch_kv_append(const KvAppendParams& p0, cudaStream_t s) {
     KvAppendParams p = p0;
-    p.tile = append_tile_rows(p.T);
+    p.tile = append_tile_rows(p.T, 1 << p.log2_page);
     const dim3 grid((unsigned)((p.T + p.tile - 1) / p.tile), (unsigned)p.Hkv, 2);
     const int chunks = ((1 << p.log2_page) * p.d) / (8 * kAppendThreads);  // a whole page's, for each thread
     switch (chunks) {
