@@ -163,7 +163,12 @@ constexpr int kAppendThreads = 256;
 constexpr int kAppendWarps = kAppendThreads / 32;
 constexpr int kAppendShort = 4;  // rows that one warp takes
 
-__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7fff7fffu); }
+// The larger magnitudes of two bf16 pairs (m's not negative); NaN stays.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t w) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(w & 0x7fff7fffu));
+    return r;
+}
 
 // 8 bf16 (packed) times f to 8 e4m3 codes; values that are not finite give 0.
 __device__ __forceinline__ uint2 codes8(uint4 x, float f, bool finite) {
@@ -206,26 +211,35 @@ __device__ __forceinline__ void append_run(const KvAppendParams& p, int t, int n
                                            int threads, Max&& reduce_max) {
     const uint16_t* src = (is_v ? p.v : p.k) + (int64_t)head * p.d;
     const int64_t ld = is_v ? p.ldv : p.ldk;
-    const int per_row = p.d >> 3, chunks = n * per_row, shift = p.d == 256 ? 5 : 4;
+    const int per_row = p.d >> 3, shift = p.d == 256 ? 5 : 4;
     const int64_t page = slot >> p.log2_page;
     const int at = (int)(slot & ((1 << p.log2_page) - 1));
     float* scale = (is_v ? p.v_scale : p.k_scale) + page * p.Hkv + head;
     uint8_t* block = (is_v ? p.v_cache : p.k_cache) + ((page * p.Hkv + head) << p.log2_page) * p.d;
     const float old = at > 0 ? *scale : 0.0f;  // read before the maximum's barrier, replaced after it
+    // chunk who + i * threads: row r0 + i * step of the run, always the same columns
+    const int r0 = who >> shift, step = threads >> shift;
+    const uint16_t* col = src + (who & (per_row - 1)) * 8;
     uint4 x[CH];
     uint32_t m2 = 0, missing = 0;
+    if (p.rows == nullptr) {
+        const uint16_t* from = col + (int64_t)(t + r0) * ld;
+        const int64_t stride = (int64_t)step * ld;
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-        const int c = who + i * threads;
-        x[i] = make_uint4(0, 0, 0, 0);
-        if (c < chunks) {
-            int row = t + (c >> shift);
-            if (p.rows != nullptr) row = p.rows[row];
-            if (row < 0 || row >= p.n_src) missing = 0x7f80u;  // a source row that is not there: the block's scale becomes NaN
-            else x[i] = *reinterpret_cast<const uint4*>(src + row * ld + (c & (per_row - 1)) * 8);
+        for (int i = 0; i < CH; ++i) x[i] = r0 + i * step < n ? *reinterpret_cast<const uint4*>(from + i * stride) : make_uint4(0, 0, 0, 0);
+    } else {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (r0 + i * step < n) {
+                const int row = p.rows[t + r0 + i * step];
+                if (row < 0 || row >= p.n_src) missing = 0x7f80u;  // a source row that is not there: the block's scale becomes NaN
+                else x[i] = *reinterpret_cast<const uint4*>(col + (int64_t)row * ld);
+            }
         }
-        m2 = max_abs2(max_abs2(max_abs2(max_abs2(m2, x[i].x), x[i].y), x[i].z), x[i].w);
     }
+#pragma unroll
+    for (int i = 0; i < CH; ++i) m2 = max_abs2(max_abs2(max_abs2(max_abs2(m2, x[i].x), x[i].y), x[i].z), x[i].w);
     uint32_t top = reduce_max(max(max(m2 & 0xffffu, m2 >> 16), missing));
     const bool finite = top < 0x7f80u;
     if (!finite) {
@@ -248,11 +262,10 @@ __device__ __forceinline__ void append_run(const KvAppendParams& p, int t, int n
             *q = make_uint4(shrink4(w.x, f), shrink4(w.y, f), shrink4(w.z, f), shrink4(w.w, f));
         }
     }
+    uint2* to = reinterpret_cast<uint2*>(block + (int64_t)at * p.d) + who;
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-        const int c = who + i * threads;
-        if (c < chunks) *reinterpret_cast<uint2*>(block + (int64_t)at * p.d + (int64_t)c * 8) = codes8(x[i], inv, finite);
-    }
+    for (int i = 0; i < CH; ++i)
+        if (r0 + i * step < n) to[i * threads] = codes8(x[i], inv, finite);
     if (who == 0) *scale = finite && !poisoned ? now : __int_as_float(0x7fffffff);
 }
 
