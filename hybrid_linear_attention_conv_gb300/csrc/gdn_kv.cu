@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "gdn_kv.cuh"
+#include "gdn_kv_tc.cuh"
 #include "gdn_tc.cuh"
 
 namespace gdn {
@@ -57,6 +58,7 @@ __global__ void __launch_bounds__(kPlanThreads) gdn_kv_plan_kernel(KvPlanParams 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int P = 1 << p.log2_page;
     if (tid == 0) bad = 0;
+    tc::grid_wait();
     __syncthreads();
 
     const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
@@ -276,6 +278,7 @@ __global__ void __launch_bounds__(kAppendThreads, CH > 8 ? 2 : 4) gdn_kv_append_
     const int head = blockIdx.y, t0 = blockIdx.x * p.tile, P = 1 << p.log2_page;
     const bool is_v = blockIdx.z != 0;
     const int64_t last_slot = (int64_t)p.pages << p.log2_page;
+    tc::grid_wait();
 
     // Rows t0 .. t0 + tile - 1: a row begins a run unless it follows the row
     // before it inside a page.  A run ends within P rows of its first, so the
@@ -417,8 +420,7 @@ cudaError_t launch_kv_plan(const KvPlanParams& p, cudaStream_t s) {
     if (err[dev] != cudaSuccess) return err[dev];
     // a CTA for every two rows of its threads, up to one per SM
     const int grid = std::max(1, std::min(device_sm_count(), (p.rows + 2 * kPlanThreads - 1) / (2 * kPlanThreads)));
-    gdn_kv_plan_kernel<<<grid, kPlanThreads, (size_t)p.B * 8, s>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(gdn_kv_plan_kernel, dim3((unsigned)grid), kPlanThreads, (size_t)p.B * 8, s, p);
 }
 
 cudaError_t launch_kv_append(const KvAppendParams& p0, cudaStream_t s) {
@@ -427,12 +429,11 @@ cudaError_t launch_kv_append(const KvAppendParams& p0, cudaStream_t s) {
     const dim3 grid((unsigned)((p.T + p.tile - 1) / p.tile), (unsigned)p.Hkv, 2);
     const int chunks = ((1 << p.log2_page) * p.d) / (8 * kAppendThreads);  // a whole page's, for each thread
     switch (chunks) {
-        case 2: gdn_kv_append_kernel<2><<<grid, kAppendThreads, 0, s>>>(p); break;
-        case 4: gdn_kv_append_kernel<4><<<grid, kAppendThreads, 0, s>>>(p); break;
-        case 8: gdn_kv_append_kernel<8><<<grid, kAppendThreads, 0, s>>>(p); break;
-        default: gdn_kv_append_kernel<16><<<grid, kAppendThreads, 0, s>>>(p); break;
+        case 2: return launch_dependent(gdn_kv_append_kernel<2>, grid, kAppendThreads, 0, s, p);
+        case 4: return launch_dependent(gdn_kv_append_kernel<4>, grid, kAppendThreads, 0, s, p);
+        case 8: return launch_dependent(gdn_kv_append_kernel<8>, grid, kAppendThreads, 0, s, p);
+        default: return launch_dependent(gdn_kv_append_kernel<16>, grid, kAppendThreads, 0, s, p);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace gdn

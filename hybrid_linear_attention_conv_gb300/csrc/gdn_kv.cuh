@@ -102,6 +102,24 @@ cudaError_t launch_kv_attn_tiles(KvAttnParams& p, int d, cudaStream_t s);
 size_t kv_attn_tiles_workspace(int d);
 
 #ifdef __CUDACC__
+// Every kernel of a step is launched as a programmatic dependent of the one
+// before it on the stream: its blocks may be placed while that one drains, and
+// touch no memory that it may write before tc::grid_wait().
+template <class... Args>
+cudaError_t launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // 2^e for e in the normal range.
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
 

@@ -621,22 +621,10 @@ cudaError_t launch(KvAttnParams& p, cudaStream_t s) {
     });
     if (err[dev] != cudaSuccess) return err[dev];
     const int grid = std::min(per_sm(D) * device_sm_count(), kKvMaxCtas);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, gdn_kv_attn_rows_kernel<D>, p);
+    e = launch_dependent(gdn_kv_attn_rows_kernel<D>, dim3((unsigned)grid), kThreads, smem, s, p);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(kRows * D / 512, (unsigned)grid);
-    cfg.blockDim = dim3(kJoinWarps * 32);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, gdn_kv_join_rows_kernel<D>, (const int*)p.spans, (const int64_t*)p.span_rows, (const float*)p.partials, p.out, p.lse);
+    return launch_dependent(gdn_kv_join_rows_kernel<D>, dim3(kRows * D / 512, (unsigned)grid), kJoinWarps * 32, 0, s, (const int*)p.spans,
+                            (const int64_t*)p.span_rows, (const float*)p.partials, p.out, p.lse);
 }
 
 }  // namespace

@@ -165,6 +165,12 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
     Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
+    if (tid == 0) {
+        tc::prefetch_map(&p.tm_k);
+        tc::prefetch_map(&p.tm_v);
+    }
+    tc::grid_wait();  // nothing above touches memory that an earlier kernel may write
+
     // ---- this CTA's part of the list
     const int per = (p.B + kThreads - 1) / kThreads;
     const int rb0 = min(tid * per, p.B), rb1 = min(rb0 + per, p.B);
@@ -835,8 +841,7 @@ cudaError_t launch(KvAttnParams& p, cudaStream_t s) {
     });
     if (err[dev] != cudaSuccess) return err[dev];
     const int grid = std::min(device_sm_count(), kKvMaxCtas);
-    gdn_kv_attn_tiles_kernel<D><<<grid, kThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(gdn_kv_attn_tiles_kernel<D>, dim3((unsigned)grid), kThreads, smem, s, p);
 }
 
 }  // namespace
