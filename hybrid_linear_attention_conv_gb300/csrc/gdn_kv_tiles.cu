@@ -49,7 +49,7 @@ constexpr float kPExp = 5.0f;           // weights are held times 2^5
 constexpr float kGrow = 3.8f;           // 2^(5 + 3.8) = 446
 constexpr int kScaleRing = 8;
 constexpr int kSoftRegs = 88, kOtherRegs = 64;  // 512 x 88 + 256 x 64 = 768 x 80
-constexpr int kItemCost = 4;            // an item's beginning and end, in tiles
+constexpr int kItemCost = 6;            // an item's beginning and end, in tiles
 constexpr int kMinTiles = 8;            // what a CTA takes at least
 constexpr uint64_t kDrainNs = 200000000ull;
 
@@ -60,6 +60,7 @@ struct TilesSmem {
     static constexpr int kBufs = D == 256 ? 2 : 3;            // tiles of logits in tensor memory
     static constexpr int kQBufs = D == 256 ? 1 : 2;           // items' q
     static constexpr bool kTwo = D == 128;                    // two warps issue MMAs
+    static constexpr bool kEarly = D == 256;                  // the product starts on half the weights
     alignas(1024) uint8_t q[kQBufs][2][kM * D];               // hi, lo
     alignas(1024) uint8_t ring[kSlots][kSlot];
     float4 scales[kScaleRing][4];                             // of 32 tokens: key scale, log2 of the value scale, 1 / value scale
@@ -68,7 +69,7 @@ struct TilesSmem {
     float top[2][2][2][kM];                                   // by team and half: the rows' maxima of two tiles in turn
     float ml[2][2][kM], mr[2][2][2][kM];                      // by item: the teams' references; each half's sum
     alignas(16) uint8_t stage[kSoftWarps][32 * 32];           // a warp's 32 rows x 16 columns of output on their way out
-    alignas(8) uint64_t full[kSlots], empty[kSlots], s_full[kBufs], p_ready[kBufs], o_done[kBufs], scales_full[kScaleRing];
+    alignas(8) uint64_t full[kSlots], empty[kSlots], s_full[kBufs], p_ready[2][kBufs], o_done[kBufs], scales_full[kScaleRing];
     uint64_t q_full[kQBufs], q_empty[kQBufs], item_done, o_free, drained;
     long long scan[kThreads / 32];
     int qbase[kThreads];
@@ -157,7 +158,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __grid_constant__ KvAttnParams p) {
     using Smem = TilesSmem<D>;
     constexpr int kSlot = Smem::kSlot, kSlots = Smem::kSlots, kBufs = Smem::kBufs, kQBufs = Smem::kQBufs, kHalves = D / 128;
-    constexpr bool kTwo = Smem::kTwo;
+    constexpr bool kTwo = Smem::kTwo, kEarly = Smem::kEarly;
     constexpr int kQ = kTwo ? kQWarps - 1 : kQWarps;  // warps that split q
     constexpr uint32_t kHalfBytes = kN * 128;
     constexpr int kPart = kM * D + 2 * kM;
@@ -261,6 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
             tc::mbar_init(s_full + 8 * i, 1);
             tc::mbar_init(o_done + 8 * i, 1);
             tc::mbar_init(p_ready + 8 * i, kTeamWarps);
+            tc::mbar_init(p_ready + 8 * (kBufs + i), kTeamWarps);
         }
         for (int i = 0; i < kScaleRing; ++i) tc::mbar_init(scales_full + 8 * i, 1);
         for (int i = 0; i < kQBufs; ++i) {
@@ -398,16 +400,27 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
             const int u = 2 * g + 1, slot = u % kSlots, buf = g % kBufs;
             if (first && item > 0) wait(o_free, item - 1);
             wait(full + 8 * slot, u / kSlots);
-            wait(p_ready + 8 * buf, g / kBufs);
-            tc::fence_after_sync();
             const uint64_t v = tc::smem_desc_mn_sw128(ring + slot * kSlot, kHalfBytes);
             const uint32_t a = tmem + buf * kN;
+            // kEarly: the weights come in two halves, of tokens 0 .. 31 and 64 .. 95 first, and the
+            // product of those runs while the others' exponentials do (d = 256: 529 -> 511 us for 1,024
+            // queries after 30,000 tokens; d = 128, where the softmax is the longer, 369 -> 388 us)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                if (kEarly || c == 0) {
+                    wait(p_ready + 8 * (c * kBufs + buf), g / kBufs);
+                    tc::fence_after_sync();
+                }
+                if (tc::elect_one()) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+#pragma unroll
+                        for (int part = 0; part < 2; ++part)
+                            tc::mma_e4m3_ts(tO, a + half * 64 + c * 8 + part * 16, v + ((2 * half + c) * 32 * 128 >> 4), id_o, c + half + part > 0 || !first);
+                }
+                __syncwarp();
+            }
             if (tc::elect_one()) {
-#pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int ks = 0; ks < kN / 32; ++ks)
-                        tc::mma_e4m3_ts(tO, a + (ks >> 1) * 64 + (ks & 1) * 8 + part * 16, v + (ks * 32 * 128 >> 4), id_o, part + ks > 0 || !first);
                 tc::mma_commit(empty + 8 * slot);
                 tc::mma_commit(o_done + 8 * buf);
                 if (last) tc::mma_commit(item_done);
@@ -651,6 +664,16 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                     }
                 }
 
+                if (j * kN + kN > w.r.L) {  // whatever lies past the end: zeros for the product
+                    const int u = 2 * g + 1, slot = u % kSlots;
+                    wait(full + 8 * slot, u / kSlots);
+                    const int first = max(0, w.r.L - j * kN);
+                    for (int i = half * kM + local; i < (kN - first) * (D / 16); i += 2 * kM) {
+                        const int tok = first + i / (D / 16), cc = i % (D / 16);
+                        *reinterpret_cast<uint4*>(sm.ring[slot] + (cc >> 3) * kHalfBytes + tok * 128 + (cc & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    tc::fence_async_smem();
+                }
                 // ---- weights
                 const float shift = kPExp - (m == -INFINITY ? 0.0f : m);
 #pragma unroll 1
@@ -686,21 +709,13 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                     // a row that sees nothing here takes nothing from the block's scale
                     const float sum = part[0] + part[1];
                     if (sum != 0.0f) l = fmaf(sum, c ? sc1.z : sc0.z, l);
-                }
-                if (j * kN + kN > w.r.L) {  // whatever lies past the end: zeros for the product
-                    const int u = 2 * g + 1, slot = u % kSlots;
-                    wait(full + 8 * slot, u / kSlots);
-                    const int first = max(0, w.r.L - j * kN);
-                    for (int i = half * kM + local; i < (kN - first) * (D / 16); i += 2 * kM) {
-                        const int tok = first + i / (D / 16), cc = i % (D / 16);
-                        *reinterpret_cast<uint4*>(sm.ring[slot] + (cc >> 3) * kHalfBytes + tok * 128 + (cc & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    if (kEarly || c == 1) {
+                        tc::tmem_wait_st();
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(p_ready + 8 * ((kEarly ? c : 0) * kBufs + buf));
                     }
-                    tc::fence_async_smem();
                 }
-                tc::tmem_wait_st();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(p_ready + 8 * buf);
             }
 
             // ---- the item's output: whole, or this CTA's part of it.  A team and half has a quarter of the columns.
@@ -717,31 +732,29 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
             }
             const long long tile0 = w.x - w.v0 + kItemCost;  // the place of the item's first tile
             const int c0 = (int)(tile0 / W), c1 = (int)((tile0 + w.kt - 1) / W);
-            // 32 columns from col0 + 32 k of the warp's 32 rows, sixteen at a time through
-            // shared memory: a row's 32 bytes then leave from two lanes (a thread storing its
-            // own row would touch 32 lines with every instruction).
+            // Sixteen columns from `col` of the warp's 32 rows, through shared memory: a row's
+            // 32 bytes then leave from two lanes (a thread storing its own row would touch 32
+            // lines with every instruction).  Called from rolled loops: between two items this
+            // code has left the instruction caches, and its fetch is most of its time.
             const int rows_here = min(kM, w.r.n * p.G - w.t * kM);
-            auto put = [&](int k, const float (&o)[32], float inv) {
+            auto put = [&](int col, const float (&o)[16], float inv) {
                 uint4* stage = reinterpret_cast<uint4*>(sm.stage[warp]);
+                __syncwarp();
 #pragma unroll
-                for (int h2 = 0; h2 < 2; ++h2) {
-                    __syncwarp();
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t u[4];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t u[4];
+                    for (int e = 0; e < 4; ++e)
+                        u[e] = tc::pack_bf16(__float2bfloat16_rn(o[8 * i + 2 * e] * inv), __float2bfloat16_rn(o[8 * i + 2 * e + 1] * inv));
+                    stage[lane * 2 + (i ^ ((lane >> 2) & 1))] = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+                __syncwarp();
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            u[e] = tc::pack_bf16(__float2bfloat16_rn(o[16 * h2 + 8 * i + 2 * e] * inv), __float2bfloat16_rn(o[16 * h2 + 8 * i + 2 * e + 1] * inv));
-                        stage[lane * 2 + (i ^ ((lane >> 2) & 1))] = make_uint4(u[0], u[1], u[2], u[3]);
-                    }
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int r = i * 16 + (lane >> 1);
-                        const int64_t to = __shfl_sync(~0u, at, r);
-                        if (quad * 32 + r < rows_here)
-                            reinterpret_cast<uint4*>(p.out + to * D + col0 + 32 * k + 16 * h2)[lane & 1] = stage[r * 2 + ((lane & 1) ^ ((r >> 2) & 1))];
-                    }
+                for (int i = 0; i < 2; ++i) {
+                    const int r = i * 16 + (lane >> 1);
+                    const int64_t to = __shfl_sync(~0u, at, r);
+                    if (quad * 32 + r < rows_here)
+                        reinterpret_cast<uint4*>(p.out + to * D + col)[lane & 1] = stage[r * 2 + ((lane & 1) ^ ((r >> 2) & 1))];
                 }
             };
             auto put_lse = [&]() {
@@ -753,21 +766,21 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
             if (c0 == c1) {
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no token seen: zeros
 #pragma unroll 1
-                for (int k = 0; k < D / 128; ++k) {
-                    float o[32];
-                    tc::tmem_ld32(tO + lanes + col0 + 32 * k, o);
-                    put(k, o, inv);
+                for (int k = 0; k < D / 64; ++k) {
+                    float o[16];
+                    tc::tmem_ld16(tO + lanes + col0 + 16 * k, o);
+                    put(col0 + 16 * k, o, inv);
                 }
                 put_lse();
             } else {
                 float* part = p.partials + ((size_t)blockIdx.x * 2 + (w.j0 == 0 ? 1 : 0)) * kPart;
 #pragma unroll 1
-                for (int k = 0; k < D / 128; ++k) {
-                    float o[32];
-                    tc::tmem_ld32(tO + lanes + col0 + 32 * k, o);
+                for (int k = 0; k < D / 64; ++k) {
+                    float o[16];
+                    tc::tmem_ld16(tO + lanes + col0 + 16 * k, o);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        reinterpret_cast<float4*>(part)[(col0 / 4 + 8 * k + i) * kM + local] =
+                    for (int i = 0; i < 4; ++i)
+                        reinterpret_cast<float4*>(part)[(col0 / 4 + 4 * k + i) * kM + local] =
                             make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                 }
                 if (part_id == 0) {
@@ -799,22 +812,23 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                         l = fmaf(__ldcg(part_of(c) + kM * D + kM + local), factor(__ldcg(part_of(c) + kM * D + local), m), l);
                     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
-                    for (int k = 0; k < D / 128; ++k) {
-                        float o[32];
+                    for (int k = 0; k < D / 64; ++k) {
+                        float o[16];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+                        for (int i = 0; i < 16; ++i) o[i] = 0.0f;
+#pragma unroll 2
                         for (int c = c0; c <= c1; ++c) {
                             const float fc = factor(__ldcg(part_of(c) + kM * D + local), m);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float4 x = __ldcg(reinterpret_cast<const float4*>(part_of(c)) + (col0 / 4 + 8 * k + i) * kM + local);
+                            for (int i = 0; i < 4; ++i) {
+                                const float4 x = __ldcg(reinterpret_cast<const float4*>(part_of(c)) + (col0 / 4 + 4 * k + i) * kM + local);
                                 o[4 * i] = fmaf(x.x, fc, o[4 * i]);
                                 o[4 * i + 1] = fmaf(x.y, fc, o[4 * i + 1]);
                                 o[4 * i + 2] = fmaf(x.z, fc, o[4 * i + 2]);
                                 o[4 * i + 3] = fmaf(x.w, fc, o[4 * i + 3]);
                             }
                         }
-                        put(k, o, inv);
+                        put(col0 + 16 * k, o, inv);
                     }
                     put_lse();
                 }
