@@ -61,7 +61,7 @@ __host__ __device__ constexpr int ring_bytes(int d) { return d == 256 ? 24 * 102
 constexpr float kPScale = 8.0f;         // weights are held times 2^8
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr int kItemCost = 8;            // an item's beginning and end, in tiles
-constexpr int kMinTiles = 16;           // what a CTA takes at least
+constexpr int kMinTiles = 8;            // what a CTA takes at least
 
 template <int D>
 struct RowsSmem {

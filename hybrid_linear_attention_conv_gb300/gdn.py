@@ -818,12 +818,14 @@ def kv_plan(lens, new, held, free_pages, free_count, table, page, rows, out=None
         e, dev = torch.empty, table.device
         out = (e(b1, dtype=i32, device=dev), e(b1, dtype=i32, device=dev), e(one, dtype=i32, device=dev),
                e((B + 1,), dtype=i32, device=dev), e((rows,), dtype=torch.int64, device=dev), e(one, dtype=i32, device=dev))
+        ptrs = [t.data_ptr() for t in out]
+    else:
+        names = ("lens_out", "held_out", "free_count_out", "start", "slots", "status")
+        shapes = (b1, b1, one, (B + 1,), (rows,), one)
+        ptrs = [_ptr(t, torch.int64 if n == "slots" else i32, n, sh) for t, n, sh in zip(out, names, shapes)]
     rc = load().gdn_kv_plan(_kv_shape(B, 1, 1, 128, int(page), 0, width), _ptr(lens, i32, "lens", b1), _ptr(new, i32, "new", b1),
                             _ptr(held, i32, "held", b1), _ptr(free_pages, i32, "free_pages", (free_pages.numel(),)), free_pages.numel(),
-                            _ptr(free_count, i32, "free_count", one), _ptr(table, i32, "table", (B, width)), int(rows),
-                            _ptr(out[0], i32, "lens_out", b1), _ptr(out[1], i32, "held_out", b1), _ptr(out[2], i32, "free_count_out", one),
-                            _ptr(out[3], i32, "start", (B + 1,)), _ptr(out[4], torch.int64, "slots", (rows,)), _ptr(out[5], i32, "status", one),
-                            _raw_stream())
+                            _ptr(free_count, i32, "free_count", one), _ptr(table, i32, "table", (B, width)), int(rows), *ptrs, _raw_stream())
     if rc:
         _check(rc, "gdn_kv_plan")
     return out

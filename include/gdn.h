@@ -738,10 +738,15 @@ size_t gdn_kv_attention_workspace_bytes(const gdn_kv_shape* shape);
  *          next one needs it.  Calls that may overlap need workspaces of their own.
  *          Its int32 at offset 0 is set non-zero if a bounded device wait
  *          gave up, and stays so; gdn_kv_attention_status() reads it.
- * Products are exact in the codes; q and the softmax's weights are held as
- * two e4m3 numbers each (eight significant bits: bf16's), sums in fp32.  What
- * lies in the cache past a request's length is never used, whatever its bits.
- * Results do not depend on timing: the same call gives the same bits.
+ * Products are exact in the codes, sums are fp32.  q, times a power of two for
+ * each row, is exact while within 2^-10 of the row's largest; a softmax weight
+ * is within 2^-8 of itself (two e4m3 numbers), or 2^-11 (f16).  What lies in
+ * the cache past a request's length is never used, whatever its bits.
+ * T picks the kernel: eight rows (queries x heads of a group) at a time while
+ * there are at most eight a request, T * Hq / Hkv <= 8 * B, and 128 above; the
+ * two differ in last bits.  Results do not depend on timing: the same call gives
+ * the same bits.
+ * The kernels are programmatic dependent launches, as gdn_conv_decode_step's.
  */
 int gdn_kv_attention(const gdn_kv_shape* shape, int32_t T, const gdn_bf16* q, int64_t ldq, const uint8_t* k_cache,
                      const uint8_t* v_cache, const float* k_scale, const float* v_scale, const int32_t* table,
