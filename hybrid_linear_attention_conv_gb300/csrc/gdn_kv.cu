@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "gdn_kv.cuh"
@@ -402,9 +403,28 @@ bool encode_cache_map(CUtensorMap* map, const uint8_t* cache, const gdn_kv_shape
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Which attention kernel: eight rows at a time, or 128.  The first reads a
-// request's cache once for every eight of its rows (queries x heads of a group).
-bool use_tiles(const gdn_kv_shape* s, int T) { return (int64_t)T * (s->Hq / s->Hkv) > (int64_t)8 * s->B; }
+// Which attention kernel: eight rows (queries x heads of a group) at a time over
+// tiles of 32 tokens, which reads a request's cache once for every eight of its
+// rows, or 128 rows over tiles of 128.  Both sides' times, in tiles of the first
+// (2.6 ns of the whole GPU for d = 256, 1.3 for 128): a tile of the second takes
+// 5 of them (d = 256) or 6.5, an item's beginning and end 8 tiles of the first
+// and 6 of the second, and a launch of the second 3 << 20 / d more where its
+// items are fewer than the SMs (each is spread over several CTAs and joined),
+// 1 << 20 / d where they are not.  All that the host knows of the lengths is the
+// table's width: where that bound is loose, both sides grow, and more than
+// eight rows a request go to the second.  Measured (rows, tiles, us): 64 requests of
+// 8,000 tokens, 24/4 heads of 256, 6 rows 167, 219; 12 rows 317, 220; one of
+// 8,000 tokens, 60 rows 24, 41; 252 rows 56, 43; a first prompt of 85 tokens 16, 27;
+// 64/4 heads of 128, 64 requests of 8,000, 16 rows 171, 153; over 185 such pairs
+// the rule loses 1.3x at most; eight rows a request as the border lost up to 2.8x.
+bool use_tiles(const gdn_kv_shape* s, int T) {
+    const double L = (double)s->width * s->page, heads = (double)s->B * s->Hkv;
+    const double rows = std::ceil((double)T * (s->Hq / s->Hkv) / s->B);
+    const double items = heads * std::ceil(rows / 128);
+    const double by_eight = heads * std::ceil(rows / 8) * (L / 32 + 8);
+    const double by_tiles = items * (L / 128 + 6) * (s->d == 256 ? 5.0 : 6.5) + (double)((items < device_sm_count() ? 3 << 20 : 1 << 20) / s->d);
+    return by_eight > by_tiles;
+}
 
 }  // namespace
 

@@ -742,10 +742,12 @@ size_t gdn_kv_attention_workspace_bytes(const gdn_kv_shape* shape);
  * each row, is exact while within 2^-10 of the row's largest; a softmax weight
  * is within 2^-8 of itself (two e4m3 numbers), or 2^-11 (f16).  What lies in
  * the cache past a request's length is never used, whatever its bits.
- * T picks the kernel: eight rows (queries x heads of a group) at a time while
- * there are at most eight a request, T * Hq / Hkv <= 8 * B, and 128 above; the
- * two differ in last bits.  Results do not depend on timing: the same call gives
- * the same bits.
+ * The sizes (T, the shape, and its width as the bound of the lengths) pick the
+ * kernel, eight rows (queries x heads of a group) at a time or 128; the two
+ * differ in last bits.  Up to eight rows a request, T * Hq / Hkv <= 8 * B, it is the
+ * first; above, a table no wider than the lengths need lets small steps stay
+ * with it where it is the faster.  Results do not depend on timing: the same
+ * call gives the same bits.
  * The kernels are programmatic dependent launches, as gdn_conv_decode_step's.
  */
 int gdn_kv_attention(const gdn_kv_shape* shape, int32_t T, const gdn_bf16* q, int64_t ldq, const uint8_t* k_cache,

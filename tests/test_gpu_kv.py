@@ -324,21 +324,26 @@ class Step:
         self.tree = torch.tensor([w - (1 << 64) if w >> 63 else w for w in words], dtype=torch.int64, device=DEV)
         return self
 
-    def run(self, scale=None, workspace=None, pad=2):
-        """pad: rows of q past the requests' own.  The number of rows picks the kernel (eight rows
-        at a time up to eight a request and key/value head, 128 above), so pad=0 and pad=2 of a few
-        single tokens run both."""
+    def run(self, scale=None, workspace=None, tiles=False, pad=2):
+        """pad: rows of q past the requests' own.  The rows a request and the table's width, which
+        bounds the contexts, pick the kernel: tiles adds enough of both for the one of 128 rows at a
+        time; without it few rows go to the one of eight."""
+        table, B = self.table, len(self.L)
+        if tiles:
+            pad = 9 * B
+            more = ((1 << 22) // (B * self.Hkv) + 8192) // self.page
+            table = torch.cat([table, table.new_full((B, more), -1)], 1)
         out = torch.full((self.T + pad, self.Hq, self.d), 7.0, dtype=torch.bfloat16, device=DEV)  # rows that no request has stay
         lse = torch.full((self.T + pad, self.Hq), 7.0, device=DEV)
         q = torch.cat([self.q, self.q.new_zeros((pad, self.Hq, self.d))])
         tree = None if self.tree is None else torch.cat([self.tree, self.tree.new_zeros(pad)])
-        gdn.kv_attention(q, *self.cache, self.table, self.start, self.lens, scale=scale, tree=tree, out=out, lse=lse, workspace=workspace)
+        gdn.kv_attention(q, *self.cache, table, self.start, self.lens, scale=scale, tree=tree, out=out, lse=lse, workspace=workspace)
         torch.cuda.synchronize()
         assert (out[self.T:] == 7.0).all() and (lse[self.T:] == 7.0).all()
         return out[:self.T], lse[:self.T]
 
-    def check(self, scale=None, got=None, pad=2):
-        out, lse = got or self.run(scale, pad=pad)
+    def check(self, scale=None, got=None, tiles=False):
+        out, lse = got or self.run(scale, tiles=tiles)
         scale = self.d ** -0.5 if scale is None else scale
         G = self.Hq // self.Hkv
         kc, vc = (c.view(torch.uint8) for c in self.cache[:2])
@@ -394,49 +399,53 @@ SHAPES = [(24, 4, 256), (8, 8, 128), (16, 2, 128), (3, 1, 256), (32, 8, 128), (1
 
 @pytest.mark.parametrize("Hq,Hkv,d", SHAPES)
 @pytest.mark.parametrize("page", [32, 64, 128])
-@pytest.mark.parametrize("pad", [0, 200])
-def test_attention_one_token(Hq, Hkv, d, page, pad):
+@pytest.mark.parametrize("tiles", [False, True])
+def test_attention_one_token(Hq, Hkv, d, page, tiles):
     lens = [1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 500, 1025]
-    Step(lens, [1] * len(lens), Hq, Hkv, d, page, seed=page + d).check(pad=pad)
+    Step(lens, [1] * len(lens), Hq, Hkv, d, page, seed=page + d).check(tiles=tiles)
 
 
 @pytest.mark.parametrize("Hq,Hkv,d", SHAPES)
-def test_attention_prompts_and_single_tokens(Hq, Hkv, d):
-    Step([40, 7, 300, 129, 1, 513, 64, 0], [40, 1, 130, 0, 1, 5, 64, 0], Hq, Hkv, d, 64, seed=d).check()
+@pytest.mark.parametrize("tiles", [False, True])
+def test_attention_prompts_and_single_tokens(Hq, Hkv, d, tiles):
+    Step([40, 7, 300, 129, 1, 513, 64, 0], [40, 1, 130, 0, 1, 5, 64, 0], Hq, Hkv, d, 64, seed=d).check(tiles=tiles)
 
 
 @pytest.mark.parametrize("Hq,Hkv,d", [(24, 4, 256), (8, 8, 128), (16, 1, 128)])
 @pytest.mark.parametrize("n", [1, 2, 7, 32, 63, 64])
-def test_attention_trees(Hq, Hkv, d, n):
-    Step([n, n + 1, n + 31, n + 700], [n] * 4, Hq, Hkv, d, 32, seed=n).with_trees(n).check()
+@pytest.mark.parametrize("tiles", [False, True])
+def test_attention_trees(Hq, Hkv, d, n, tiles):
+    Step([n, n + 1, n + 31, n + 700], [n] * 4, Hq, Hkv, d, 32, seed=n).with_trees(n).check(tiles=tiles)
 
 
-def test_attention_tree_of_more_nodes_than_bits():
-    Step([70, 200], [70, 66], 8, 2, 128, 64, seed=3).with_trees().check()
+@pytest.mark.parametrize("tiles", [False, True])
+def test_attention_tree_of_more_nodes_than_bits(tiles):
+    Step([70, 200], [70, 66], 8, 2, 128, 64, seed=3).with_trees().check(tiles=tiles)
 
 
-def test_attention_rows_that_see_nothing():
+@pytest.mark.parametrize("tiles", [False, True])
+def test_attention_rows_that_see_nothing(tiles):
     """More queries than tokens: the first of them see none."""
     s = Step([3, 0, 40, 0], [5, 2, 41, 1], 8, 2, 128, 32, seed=4)
-    out, lse = s.check()
+    out, lse = s.check(tiles=tiles)
     assert (out[:2] == 0).all() and torch.isneginf(lse[:2]).all() and (out[5:7] == 0).all()
     s = Step([30, 64], [30, 3], 6, 1, 256, 32, seed=5).with_trees()
     s.tree[:] = 0
-    out, lse = s.check()
+    out, lse = s.check(tiles=tiles)
     assert (out[:30] == 0).all() and torch.isneginf(lse[:30]).all() and torch.isfinite(lse[30:]).all()
 
 
 @pytest.mark.parametrize("sharp,v_exp", [(8.0, (-9, -5)), (0.01, (-9, -5)), (1.0, (-60, 40)), (30.0, (-20, 20))])
 @pytest.mark.parametrize("new", [1, 150])
 def test_attention_peaked_flat_and_mixed_scales(sharp, v_exp, new):
-    for pad in (0, 2):
-        Step([2000, 555], [new, min(new, 20)], 12, 2, 128, 64, seed=8, sharp=sharp, v_exp=v_exp).check(pad=pad)
-        Step([700], [new], 6, 1, 256, 128, seed=9, sharp=sharp, v_exp=v_exp).check(pad=pad)
+    for tiles in (False, True):
+        Step([2000, 555], [new, min(new, 20)], 12, 2, 128, 64, seed=8, sharp=sharp, v_exp=v_exp).check(tiles=tiles)
+        Step([700], [new], 6, 1, 256, 128, seed=9, sharp=sharp, v_exp=v_exp).check(tiles=tiles)
 
 
 def test_attention_growing_maximum():
     """Logits that rise along the context: every tile brings a new maximum."""
-    for new, pad in ((1, 0), (1, 2), (140, 2)):
+    for new, tiles in ((1, False), (1, True), (140, False), (140, True)):
         s = Step([3000], [new], 8, 1, 128, 64, seed=10)
         ramp = torch.linspace(0, 400, 64 * 48, device=DEV)[:s.page * s.table.shape[1]]
         s.q = torch.zeros_like(s.q)
@@ -446,35 +455,36 @@ def test_attention_growing_maximum():
             s.cache[0][pg, 0, :, 0] = ramp[j * 64:(j + 1) * 64].to(torch.float8_e4m3fn)
         s.cache[0].view(torch.uint8).masked_fill_(~s.owned[:, None, :, None], NAN_CODE)
         s.cache[2].fill_(1.0)
-        s.check(scale=0.5, pad=pad)
+        s.check(scale=0.5, tiles=tiles)
 
 
 @pytest.mark.parametrize("Hq,Hkv,d,new", [(24, 4, 256, 1), (24, 4, 256, 32), (8, 2, 128, 1), (32, 8, 128, 700)])
-@pytest.mark.parametrize("pad", [0, 2])
-def test_attention_long_context_and_same_bits(Hq, Hkv, d, new, pad):
+@pytest.mark.parametrize("tiles", [False, True])
+def test_attention_long_context_and_same_bits(Hq, Hkv, d, new, tiles):
     s = Step([20011], [new], Hq, Hkv, d, 64, seed=12)
     ws = torch.zeros(gdn.kv_attention_workspace_bytes(Hq, Hkv, d), dtype=torch.uint8, device=DEV)
-    first = s.check(got=s.run(workspace=ws, pad=pad))
+    first = s.check(got=s.run(workspace=ws, tiles=tiles))
     for _ in range(3):
-        again = s.run(workspace=ws, pad=pad)
+        again = s.run(workspace=ws, tiles=tiles)
         assert torch.equal(first[0].view(torch.int16), again[0].view(torch.int16)) and torch.equal(first[1], again[1])
     assert gdn.kv_attention_status(ws) == 0
 
 
 def test_attention_many_requests():
     lens = [(37 * i) % 700 for i in range(300)]
-    for pad in (0, 2000):
-        Step(lens, [1 if x else 0 for x in lens], 8, 2, 128, 32, seed=13).check(pad=pad)
+    for tiles in (False, True):
+        Step(lens, [1 if x else 0 for x in lens], 8, 2, 128, 32, seed=13).check(tiles=tiles)
 
 
-@pytest.mark.parametrize("new,pad", [(1, 0), (1, 2), (40, 2)])
-def test_attention_not_a_number_stays_in_its_rows(new, pad):
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("tiles", [False, True])
+def test_attention_not_a_number_stays_in_its_rows(new, tiles):
     s = Step([200, 90], [new, 1], 16, 2, 128, 64, seed=14)
-    clean = s.run(pad=pad)
+    clean = s.run(tiles=tiles)
     # a query
     q = s.q.clone()
     s.q[new // 2, 3, 5] = math.inf
-    out, lse = s.run(pad=pad)
+    out, lse = s.run(tiles=tiles)
     rows = torch.zeros(out.shape[:2], dtype=torch.bool, device=DEV)
     rows[new // 2, 3] = True
     assert torch.isnan(out[rows]).all() and torch.isnan(lse[rows]).all()
@@ -484,7 +494,7 @@ def test_attention_not_a_number_stays_in_its_rows(new, pad):
     for which in (2, 3):
         keep = s.cache[which].clone()
         s.cache[which][int(s.table[0, 3]), 1] = math.nan
-        out, lse = s.run(pad=pad)
+        out, lse = s.run(tiles=tiles)
         rows[:] = False
         for i in range(new):
             if 200 - new + i >= 192:
@@ -496,7 +506,7 @@ def test_attention_not_a_number_stays_in_its_rows(new, pad):
     for entry in (-1, s.pages, 2 ** 31 - 1, -2 ** 31):
         keep = s.table.clone()
         s.table[0, 3] = entry
-        out, lse = s.run(pad=pad)
+        out, lse = s.run(tiles=tiles)
         rows[:] = False
         for i in range(new):
             if 200 - new + i >= 192:
@@ -508,7 +518,7 @@ def test_attention_not_a_number_stays_in_its_rows(new, pad):
 def test_attention_length_past_the_table_is_cut():
     """lens beyond the table's width: what the table has counts, and nothing else is read."""
     s = Step([64, 64], [1, 1], 8, 2, 128, 32, seed=15, spare_width=0)
-    for pad in (0, 2):
+    for pad in (0, 6000):  # of so many rows the kernel of 128 at a time takes any table's
         s.lens = i32([64, 64])
         ref = s.run(pad=pad)
         s.lens = i32([64, 10 ** 9])
@@ -518,7 +528,7 @@ def test_attention_length_past_the_table_is_cut():
 
 def test_attention_on_another_stream_and_in_a_graph():
     s = Step([900, 33], [1, 1], 24, 4, 256, 64, seed=16)
-    ref = s.run(pad=0)
+    ref = s.run()
     side = torch.cuda.Stream()
     ws = torch.zeros(gdn.kv_attention_workspace_bytes(24, 4, 256), dtype=torch.uint8, device=DEV)
     out = torch.empty_like(s.q)
@@ -540,11 +550,11 @@ def test_attention_on_another_stream_and_in_a_graph():
     s.L = [800, 20]
     graph.replay()
     torch.cuda.synchronize()
-    assert torch.equal(out, s.run(pad=0)[0])
+    assert torch.equal(out, s.run()[0])
 
 
-@pytest.mark.parametrize("new,pad", [(1, 0), (100, 2)])
-def test_attention_timeout_is_readable_and_recovers(new, pad):
+@pytest.mark.parametrize("new,tiles", [(1, False), (100, True)])
+def test_attention_timeout_is_readable_and_recovers(new, tiles):
     """A wait limit of 0 makes the waits for copies just requested give up at their first
     empty probe (over a context whose copies cannot all have landed by the time they are
     waited for); the kernel still lets them land before it ends."""
@@ -552,12 +562,12 @@ def test_attention_timeout_is_readable_and_recovers(new, pad):
     ws = torch.zeros(gdn.kv_attention_workspace_bytes(24, 4, 256), dtype=torch.uint8, device=DEV)
     prev = gdn.set_wait_limit_ns(0)
     try:
-        s.run(workspace=ws, pad=pad)
+        s.run(workspace=ws, tiles=tiles)
         assert gdn.kv_attention_status(ws) != 0
     finally:
         gdn.set_wait_limit_ns(prev)
     ws.zero_()
-    s.check(got=s.run(workspace=ws, pad=pad))
+    s.check(got=s.run(workspace=ws, tiles=tiles))
     assert gdn.kv_attention_status(ws) == 0
 
 
