@@ -26,6 +26,8 @@ namespace {
 // share of the outputs, so nothing waits on another CTA.  A slot takes its page from
 // the table's old entries or straight from the free stack, never from the
 // entries this launch writes.
+// Bound by latency, a chain of five dependent reads: in a graph 2.9 us for 64
+// requests of one token, 5.6 us for 1,500 requests and 45,000 tokens.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 512;
 constexpr int kPlanMaxB = 12288;  // 2 x 4 bytes a request of shared memory
@@ -161,6 +163,11 @@ __global__ void __launch_bounds__(kPlanThreads) gdn_kv_plan_kernel(KvPlanParams 
 // warp take each short run, and takes the long ones as a whole, a thread
 // holding its part of the run in registers between the maximum and the
 // conversion.
+// Measured in a graph, 4 heads of 256: 64 single tokens 4.1 us; 8,192 rows
+// 10.2 us = 4.9 TB/s (a CTA's life is load, maximum, barrier, conversion, store, and
+// there are 1.7 CTAs for each that is resident: two waves, the second not full; the
+// conversion keeps the integer pipe 55 % busy).  37 chunks of up to 2,000 rows, 8 heads
+// of 128: 23.0 us = 3.5 TB/s, with pages begun and ended inside the chunks.
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 256;
 constexpr int kAppendWarps = kAppendThreads / 32;
