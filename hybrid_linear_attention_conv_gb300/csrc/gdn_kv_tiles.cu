@@ -312,6 +312,61 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
     w.x = x0;
     w.x1 = x1;
 
+    // Warp me of n splits its share of the rows of v's item into q's buffer qb.
+    auto split_q = [&](const Walk& v, int qb, int me, int n, auto&& may_write) {
+        constexpr int kLanes = D / 16;              // of a row, 16 values each
+        constexpr int kAtOnce = 32 / kLanes;        // rows of a warp's step
+        constexpr int kBatch = 2;                   // steps whose loads go out together
+        const int sub = lane / kLanes, c = lane % kLanes;
+        const int rows = min(v.r.n * p.G - v.t * kM, kM);
+        const RowMap map(p, v.t);
+#pragma unroll 1
+        for (int i0 = me; i0 < kM / kAtOnce; i0 += kBatch * n) {
+            uint4 x[kBatch][2];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int local = (i0 + i * n) * kAtOnce + sub;
+                x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+                if (local < rows) {
+                    int qi, hg;
+                    map.find(local, qi, hg);
+                    const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(v.r.row0 + qi) * p.ldq + (int64_t)(v.h * p.G + hg) * D) + 2 * c;
+                    x[i][0] = src[0];
+                    x[i][1] = src[1];
+                }
+            }
+            may_write();
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int local = (i0 + i * n) * kAtOnce + sub;
+                if (i0 + i * n >= kM / kAtOnce) break;  // uniform in the warp
+                const uint32_t word[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
+                uint32_t m2 = 0;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) m2 = __vmaxu2(m2, word[k] & 0x7fff7fffu);
+                uint32_t top = max(m2 & 0xffffu, m2 >> 16);
+#pragma unroll
+                for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
+                const bool finite = top < 0x7f80u;
+                const int e = finite ? scale_exp_of_bf16(top) : 0;
+                const float inv = exp2_int(-e);
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t a = finite ? word[2 * k] : 0u, b = finite ? word[2 * k + 1] : 0u;
+                    split4_f16(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xffff0000u) * inv, __uint_as_float(b << 16) * inv,
+                               __uint_as_float(b & 0xffff0000u) * inv, hi[k], lo[k]);
+                }
+                const uint32_t at = (c >> 3) * (kM * 128) + local * 128 + (((c & 7) ^ (local & 7)) << 4);
+                *reinterpret_cast<uint4*>(sm.q[qb][0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(sm.q[qb][1] + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                // a query that is not finite makes its row NaN, through the row's factor
+                if (c == 0) sm.rf[qb][local] = finite ? exp2_int(e) * p.scale_log2 : __int_as_float(0x7fffffff);
+            }
+        }
+        tc::fence_async_smem();
+    };
+
     // Inside the branches: code after a join of the two would have to fit the smaller number.
     if (warp >= kSoftWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -484,10 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
         tc::mbar_wait(drained, 0, kDrainNs);
     } else {
         // ----------------------------------------------------------- queries
-        constexpr int kLanes = D / 16;              // of a row, 16 values each
-        constexpr int kAtOnce = 32 / kLanes;        // rows of a warp's step
-        const int sub = lane / kLanes, c = lane % kLanes;
-        constexpr int kBatch = 2;                   // steps whose loads go out together
+        // The first item's rows are split by the softmax's warps too, which have nothing to do yet.
         int item = 0;
         auto fetch = [&]() {  // an item's rows towards the L2 (a row is 2 or 4 lines)
             const int rows_next = w.r.n * p.G - w.t * kM;
@@ -503,58 +555,14 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
             }
         };
         bool more = w.settle(p);
-        if (more) fetch();
         for (; more; ++item) {
-            const int rows = w.r.n * p.G - w.t * kM;  // of this item
-            const RowMap map(p, w.t);
             const int qb = item % kQBufs;
             bool waited = item < kQBufs;
-#pragma unroll 1
-            for (int i0 = warp - kQWarp0; i0 < kM / kAtOnce; i0 += kBatch * kQ) {
-                uint4 x[kBatch][2];
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int local = (i0 + i * kQ) * kAtOnce + sub;
-                    x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
-                    if (local < min(rows, kM)) {
-                        int qi, hg;
-                        map.find(local, qi, hg);
-                        const uint4* src = reinterpret_cast<const uint4*>(p.q + (int64_t)(w.r.row0 + qi) * p.ldq + (int64_t)(w.h * p.G + hg) * D) + 2 * c;
-                        x[i][0] = src[0];
-                        x[i][1] = src[1];
-                    }
-                }
+            split_q(w, qb, warp - kQWarp0, item == 0 ? kQ + kSoftWarps : kQ, [&] {
                 if (!waited) wait(q_empty + 8 * qb, item / kQBufs - 1);
                 waited = true;
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const int local = (i0 + i * kQ) * kAtOnce + sub;
-                    if (i0 + i * kQ >= kM / kAtOnce) break;  // uniform in the warp
-                    const uint32_t word[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
-                    uint32_t m2 = 0;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) m2 = __vmaxu2(m2, word[k] & 0x7fff7fffu);
-                    uint32_t top = max(m2 & 0xffffu, m2 >> 16);
-#pragma unroll
-                    for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
-                    const bool finite = top < 0x7f80u;
-                    const int e = finite ? scale_exp_of_bf16(top) : 0;
-                    const float inv = exp2_int(-e);
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t a = finite ? word[2 * k] : 0u, b = finite ? word[2 * k + 1] : 0u;
-                        split4_f16(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xffff0000u) * inv, __uint_as_float(b << 16) * inv,
-                                   __uint_as_float(b & 0xffff0000u) * inv, hi[k], lo[k]);
-                    }
-                    const uint32_t at = (c >> 3) * (kM * 128) + local * 128 + (((c & 7) ^ (local & 7)) << 4);
-                    *reinterpret_cast<uint4*>(sm.q[qb][0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(sm.q[qb][1] + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    // a query that is not finite makes its row NaN, through the row's factor
-                    if (c == 0) sm.rf[qb][local] = finite ? exp2_int(e) * p.scale_log2 : __int_as_float(0x7fffffff);
-                }
-            }
-            tc::fence_async_smem();
+            });
+            if (item == 0) tc::named_sync(14, (kQ + kSoftWarps) * 32);
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(q_full + 8 * qb);
             w.advance(p);
@@ -577,6 +585,10 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
         Walk w_next = w;
         bool more = w_next.settle(p);
         if (more && team == 1 && half == 0) tc::named_arrive(other_bar, 96);  // there is no tile before the first
+        if (more) {
+            split_q(w_next, 0, kQ + warp, kQ + kSoftWarps, [] {});
+            tc::named_arrive(14, (kQ + kSoftWarps) * 32);
+        }
         for (; more; ++item) {
             w = w_next;
             w_next.advance(p);
