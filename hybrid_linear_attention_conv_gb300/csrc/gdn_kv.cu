@@ -603,7 +603,6 @@ int gdn_kv_attention(const gdn_kv_shape* shape, int32_t T, const gdn_bf16* q, in
     p.out = out;
     p.lse = lse;
     p.status = reinterpret_cast<int*>(ws);
-    p.counters = reinterpret_cast<unsigned*>(ws + 256);
     p.spans = reinterpret_cast<int*>(ws + kKvSpansAt);
     p.span_rows = reinterpret_cast<int64_t*>(ws + kKvSpanRowsAt);
     p.partials = reinterpret_cast<float*>(ws + kKvPartialsAt);

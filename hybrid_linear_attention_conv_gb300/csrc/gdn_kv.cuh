@@ -75,9 +75,8 @@ struct KvAttnParams {
     uint16_t* out;              // bf16 [T, Hq, d]
     float* lse;                 // [T, Hq] or nullptr
     int* status;                // workspace: the status word,
-    unsigned* counters;         // a counter for each CTA (zero between calls),
     int* spans;                 // how many CTAs further the item goes that begins in a CTA,
-    int64_t* span_rows;         // its eight rows' places in out (-1: none),
+    int64_t* span_rows;         // its eight rows' places in out (-1: none), or {first row of q, queries, row tile, head},
     float* partials;            // and the partial results
     uint64_t wait_ns;
     int64_t ldq;
@@ -86,9 +85,9 @@ struct KvAttnParams {
     unsigned group_magic;       // ceil(2^22 / G)
 };
 
-// Workspace: 256 bytes of status, the counters, spans and their rows, then the partial results.
+// Workspace: 256 bytes of status, the spans and their rows, then the partial results.
 constexpr int kKvMaxCtas = 1024;
-constexpr size_t kKvSpansAt = 256 + (size_t)kKvMaxCtas * 4;
+constexpr size_t kKvSpansAt = 256;
 constexpr size_t kKvSpanRowsAt = kKvSpansAt + (size_t)kKvMaxCtas * 4;
 constexpr size_t kKvPartialsAt = kKvSpanRowsAt + (size_t)kKvMaxCtas * 8 * 8;
 

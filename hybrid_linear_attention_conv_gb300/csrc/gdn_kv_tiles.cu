@@ -28,7 +28,8 @@
 //
 // The list of all (request, row tile, head, token tile) is cut evenly over
 // the CTAs, one to an SM, causal tiles that nobody sees left out; an item that
-// spans several CTAs is joined by the last of them to finish, in CTA order.
+// spans several CTAs leaves its parts in the workspace, and a second kernel joins
+// them, in CTA order.
 //
 // Bound by the tensor cores, 8 d flops a row and token (both products, hi and
 // lo) at twice bf16's rate, so 4 d at bf16's; for d = 128 by the softmax, whose
@@ -85,7 +86,6 @@ struct TilesSmem {
     long long scan[kThreads / 32];
     int qbase[kThreads];
     int at_b, at_t, at_h, at_v;
-    unsigned last;
     uint32_t tmem;
     int dead;
 };
@@ -165,6 +165,10 @@ struct RowMap {
 
 __device__ __forceinline__ float factor(float m, float top) { return m == top ? 1.0f : ex2(m - top); }
 
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l == 0.0f ? -INFINITY : ((m == -INFINITY ? 0.0f : m) - kPExp + log2f(l)) * 0.69314718055994531f;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __grid_constant__ KvAttnParams p) {
     using Smem = TilesSmem<D>;
@@ -182,6 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
         tc::prefetch_map(&p.tm_v);
     }
     tc::grid_wait();  // nothing above touches memory that an earlier kernel may write
+    if (tid == 0) p.spans[blockIdx.x] = 0;
 
     // ---- this CTA's part of the list
     const int per = (p.B + kThreads - 1) / kThreads;
@@ -781,8 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                 }
             };
             auto put_lse = [&]() {
-                if (p.lse != nullptr && have && part_id == 0)
-                    p.lse[at] = l == 0.0f ? -INFINITY : ((m == -INFINITY ? 0.0f : m) - kPExp + log2f(l)) * 0.69314718055994531f;
+                if (p.lse != nullptr && have && part_id == 0) p.lse[at] = lse_of(m, l);
             };
             wait(item_done, item);
             tc::fence_after_sync();
@@ -814,47 +818,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(o_free);
-            if (c0 != c1) {
-                __threadfence();
-                tc::named_sync(13, kSoftWarps * 32);
-                if (tid == 0) {
-                    const unsigned n = atomicAdd(p.counters + c0, 1u);
-                    sm.last = n == (unsigned)(c1 - c0);
-                    if (sm.last) p.counters[c0] = 0;  // as the next call finds it
-                    __threadfence();
-                }
-                tc::named_sync(13, kSoftWarps * 32);
-                const bool join = sm.last != 0;
-                tc::named_sync(13, kSoftWarps * 32);
-                if (join) {
-                    auto part_of = [&](int c) { return p.partials + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * kPart; };
-                    m = -INFINITY;
-                    for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(part_of(c) + kM * D + local));
-                    l = 0.0f;
-                    for (int c = c0; c <= c1; ++c)
-                        l = fmaf(__ldcg(part_of(c) + kM * D + kM + local), factor(__ldcg(part_of(c) + kM * D + local), m), l);
-                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll 1
-                    for (int k = 0; k < D / 64; ++k) {
-                        float o[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = 0.0f;
-#pragma unroll 2
-                        for (int c = c0; c <= c1; ++c) {
-                            const float fc = factor(__ldcg(part_of(c) + kM * D + local), m);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float4 x = __ldcg(reinterpret_cast<const float4*>(part_of(c)) + (col0 / 4 + 4 * k + i) * kM + local);
-                                o[4 * i] = fmaf(x.x, fc, o[4 * i]);
-                                o[4 * i + 1] = fmaf(x.y, fc, o[4 * i + 1]);
-                                o[4 * i + 2] = fmaf(x.z, fc, o[4 * i + 2]);
-                                o[4 * i + 3] = fmaf(x.w, fc, o[4 * i + 3]);
-                            }
-                        }
-                        put(col0 + 16 * k, o, inv);
-                    }
-                    put_lse();
-                }
+            if (c0 != c1 && w.j0 == 0 && tid == 0) {  // the item begins here: what the join needs
+                p.spans[blockIdx.x] = c1 - c0;
+                reinterpret_cast<int4*>(p.span_rows)[blockIdx.x * 4] = make_int4(w.r.row0, w.r.n, w.t, w.h);
             }
         }
     }
@@ -862,6 +828,74 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
     __syncthreads();
     tc::fence_after_sync();
     if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of the item that begins in CTA blockIdx.y and goes on in later
+// ones.  A block has 32 rows x 64 columns: four warps take the parts in turn for
+// each half of the columns, a lane a row, then each of them has eight of the columns.
+// (By the last CTA of an item, inside the kernel above, the nine parts of an item took
+// 20 us: one SM's reads, round after round.)
+template <int D>
+__global__ void __launch_bounds__(256) gdn_kv_join_tiles_kernel(const __grid_constant__ KvAttnParams p) {
+    constexpr int kPart = kM * D + 2 * kM;
+    __shared__ float acc[8][32][33];
+    __shared__ float ml[8][2][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.y;
+    tc::grid_wait();
+    const int more = p.spans[c0];
+    if (more == 0) return;
+    const int4 item = reinterpret_cast<const int4*>(p.span_rows)[c0 * 4];  // first row of q, queries, row tile, head
+    const int quad = blockIdx.x & 3, rows = item.y * p.G - item.z * kM;
+    if (quad * 32 >= rows) return;
+    const int side = warp & 1, turn = warp >> 1, local = quad * 32 + lane, col = (blockIdx.x >> 2) * 64 + side * 32;
+    float m = -INFINITY, l = 0.0f, o[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+#pragma unroll 1
+    for (int c = c0 + turn; c <= c0 + more; c += 4) {
+        const float* part = p.partials + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * kPart;
+        const float mo = part[kM * D + local], lo = part[kM * D + kM + local];
+        float4 u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = reinterpret_cast<const float4*>(part)[(col / 4 + i) * kM + local];
+        const float top = fmaxf(m, mo), a = factor(m, top), b = factor(mo, top);
+        m = top;
+        l = l * a + lo * b;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            o[4 * i] = o[4 * i] * a + u[i].x * b;
+            o[4 * i + 1] = o[4 * i + 1] * a + u[i].y * b;
+            o[4 * i + 2] = o[4 * i + 2] * a + u[i].z * b;
+            o[4 * i + 3] = o[4 * i + 3] * a + u[i].w * b;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) acc[warp][i][lane] = o[i];
+    ml[warp][0][lane] = m;
+    ml[warp][1][lane] = l;
+    __syncthreads();
+    float top = -INFINITY, total = 0.0f, v[8];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[2 * w + side][0][lane]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float f = factor(ml[2 * w + side][0][lane], top);
+        total = fmaf(ml[2 * w + side][1][lane], f, total);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = fmaf(acc[2 * w + side][8 * turn + i][lane], f, v[i]);
+    }
+    if (local >= rows) return;
+    int qi, hg;
+    RowMap(p, item.z).find(local, qi, hg);
+    const int64_t at = (int64_t)(item.x + qi) * p.Hq + item.w * p.G + hg;
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = tc::pack_bf16(__float2bfloat16_rn(v[2 * i] * inv), __float2bfloat16_rn(v[2 * i + 1] * inv));
+    *reinterpret_cast<uint4*>(p.out + at * D + col + 8 * turn) = make_uint4(u[0], u[1], u[2], u[3]);
+    if (p.lse != nullptr && col == 0 && turn == 0) p.lse[at] = lse_of(top, total);
 }
 
 template <int D>
@@ -878,7 +912,9 @@ cudaError_t launch(KvAttnParams& p, cudaStream_t s) {
     });
     if (err[dev] != cudaSuccess) return err[dev];
     const int grid = std::min(device_sm_count(), kKvMaxCtas);
-    return launch_dependent(gdn_kv_attn_tiles_kernel<D>, dim3((unsigned)grid), kThreads, smem, s, p);
+    e = launch_dependent(gdn_kv_attn_tiles_kernel<D>, dim3((unsigned)grid), kThreads, smem, s, p);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(gdn_kv_join_tiles_kernel<D>, dim3(4 * D / 64, (unsigned)grid), 256, 0, s, p);
 }
 
 }  // namespace
