@@ -420,10 +420,10 @@ bool encode_cache_map(CUtensorMap* map, const uint8_t* cache, const gdn_kv_shape
 // 1 << 20 / d where they are not.  All that the host knows of the lengths is the
 // table's width: where that bound is loose, both sides grow, and more than
 // eight rows a request go to the second.  Measured (rows, tiles, us): 64 requests of
-// 8,000 tokens, 24/4 heads of 256, 6 rows 167, 219; 12 rows 317, 220; one of
-// 8,000 tokens, 60 rows 24, 41; 252 rows 56, 43; a first prompt of 85 tokens 16, 27;
-// 64/4 heads of 128, 64 requests of 8,000, 16 rows 171, 153; over 185 such pairs
-// the rule loses 1.3x at most; eight rows a request as the border lost up to 2.8x.
+// 8,000 tokens, 24/4 heads of 256, 6 rows 165, 218; 12 rows 316, 220; one of
+// 8,000 tokens, 60 rows 25, 32; 252 rows 57, 34; a first prompt of 85 tokens 16, 27;
+// 64/4 heads of 128, 64 requests of 8,000, 16 rows 169, 150; over 199 such pairs
+// the rule loses 1.11x at most; eight rows a request as the border loses up to 2.7x.
 bool use_tiles(const gdn_kv_shape* s, int T) {
     const double L = (double)s->width * s->page, heads = (double)s->B * s->Hkv;
     const double rows = std::ceil((double)T * (s->Hq / s->Hkv) / s->B);

@@ -43,7 +43,7 @@
 //
 // Measured, 24/4 heads of 256, one token a request: 64 requests of 4,096 to 12,288
 // tokens 167 us = 6.3 TB/s of cache, 95 % of a plain copy's rate; one of 131,072 in
-// 58 us = 4.6 TB/s and of 4,097 in 11.7 us, where the chain of a launch (scan of
+// 55 us = 4.9 TB/s and of 4,097 in 11.4 us, where the chain of a launch (scan of
 // the requests, table entry, scales, first tile, join) shows.  32/8 heads of 128, 251
 // requests of up to 3,000: 133 us = 5.7 TB/s, with an item's ends once in 47 tiles.
 #include <algorithm>
@@ -635,7 +635,7 @@ cudaError_t launch(KvAttnParams& p, cudaStream_t s) {
     e = launch_dependent(gdn_kv_attn_rows_kernel<D>, dim3((unsigned)grid), kThreads, smem, s, p);
     if (e != cudaSuccess) return e;
     // Sixteen warps shorten the rounds of an item of many parts (one request of 131,072 tokens,
-    // 76 parts an item: 58.0 -> 53.9 us), where every block has a few parts or none they only take
+    // 76 parts an item: 58.0 -> 55.0 us), where every block has a few parts or none they only take
     // longer to place (64 requests: 170.2 -> 173.0).
     const int64_t items = (int64_t)p.B * p.Hkv * std::max<int64_t>(1, ((int64_t)p.T * p.G / p.B + kRows - 1) / kRows);
     const int warps = grid > 8 * items ? kJoinWarps : kJoinWarps / 2;

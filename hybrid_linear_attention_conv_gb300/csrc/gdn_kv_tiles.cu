@@ -34,11 +34,12 @@
 // Bound by the tensor cores, 8 d flops a row and token (both products, hi and
 // lo) at twice bf16's rate, so 4 d at bf16's; for d = 128 by the softmax, whose
 // exponentials and moves are the same for half the products.  Measured: a
-// prompt of 8,192, 24/4 heads of 256, causal, 606 to 639 us (by box) = 1.36 to 1.29
+// prompt of 8,192, 24/4 heads of 256, causal, 606 to 642 us (by box) = 1.36 to 1.28
 // PFLOP/s of visible pairs, about 3,000 cycles a tile of 128 x 128 against
 // 2,048 of products; 1,024 queries after 30,000 tokens 511 us = 1.53 PFLOP/s.
-// d = 128: 2,200 cycles a tile against 1,024.  Small steps pay 25 us beside
-// their tiles: the list and the first q 8 to 12, the join 7 to 9.
+// d = 128: 2,200 cycles a tile against 1,024.  Small steps pay 20 to 25 us beside
+// their tiles: the list and the first q 7 to 10, an item's beginning and end, the
+// join's launch and reads.
 #include <algorithm>
 #include <mutex>
 
@@ -833,8 +834,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
 // Joins the parts of the item that begins in CTA blockIdx.y and goes on in later
 // ones.  A block has 32 rows x 64 columns: four warps take the parts in turn for
 // each half of the columns, a lane a row, then each of them has eight of the columns.
-// (By the last CTA of an item, inside the kernel above, the nine parts of an item took
-// 20 us: one SM's reads, round after round.)
+// (By the last CTA of an item, inside the kernel above: a 64-node tree after 8,000
+// tokens, nine parts an item, 42 us instead of 34.5; eight 32-node trees 98.3 instead of 95.8; a
+// first prompt of 2,000 tokens 77 instead of 79.6, for its launch.)
 template <int D>
 __global__ void __launch_bounds__(256) gdn_kv_join_tiles_kernel(const __grid_constant__ KvAttnParams p) {
     constexpr int kPart = kM * D + 2 * kM;
