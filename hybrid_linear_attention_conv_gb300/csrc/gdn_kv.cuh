@@ -33,6 +33,29 @@ __host__ __device__ inline int32_t cache_row(int32_t page, int32_t pages, int32_
     return (int32_t)((((int64_t)page * Hkv + h) << log2_page) + (pos & ((1 << log2_page) - 1)));
 }
 
+// A worker's ring of copies: a copy's place and its barrier's phase, in turn.
+// A barrier must not be armed while its phase still awaits bytes (that is a
+// fault), so a slot is filled again only after its copy was waited for with
+// success: the first wait that gives up ends the sending for good.  The copies
+// then in flight, pending() from the slot at hand on, are waited for once more (with a
+// limit of their own), and everything after runs through on what is there.
+template <int kUnits>
+struct CopyRing {
+    int slot = 0;          // of the copy to be read next,
+    uint32_t parity = 0;   // its phase,
+    int send = 0;          // and the slot to be filled next
+    bool gave_up = false;
+    __host__ __device__ void sent() { send = send + 1 == kUnits ? 0 : send + 1; }
+    __host__ __device__ void read() {
+        if (++slot == kUnits) {
+            slot = 0;
+            parity ^= 1;
+        }
+    }
+    // Copies sent and not read, when the one at hand is among them: 1 to kUnits.
+    __host__ __device__ int pending() const { return send > slot ? send - slot : send - slot + kUnits; }
+};
+
 struct KvPlanParams {
     const int32_t* lens;        // [B] tokens cached
     const int32_t* add;         // [B] tokens to come

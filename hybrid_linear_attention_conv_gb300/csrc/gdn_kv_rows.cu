@@ -187,9 +187,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(D)) gdn_kv_attn_rows_kernel(c
         sm.at_rest = rest;
     }
     __syncthreads();
-    int slot = 0;                 // ring position and parity of the next unit to be read,
-    uint32_t parity = 0;
-    int islot = 0;                // and position of the next to be filled
+    CopyRing<kUnits> units;
 
     // The stretch at hand: request b's item `item`, tiles t0 .. t1 - 1; x is the
     // place of the list that its place v0 lies at.
@@ -233,18 +231,18 @@ __global__ void __launch_bounds__(kThreads, per_sm(D)) gdn_kv_attn_rows_kernel(c
     };
     int issued = 0;  // units
     auto issue = [&]() {
-        if (issued >= 2 * nt) return;
+        if (issued >= 2 * nt || units.gave_up) return;
         const int i = issued >> 1;
         if ((issued & 63) == 0) lookup(i);
         const int y = __shfl_sync(~0u, yI, i & 31);
         if (tc::elect_one()) {  // (a copy's operands are uniform registers: not under a test of the lane number)
             const void* map = (issued & 1) ? &p.tm_v : &p.tm_k;
-            tc::mbar_arrive_expect_tx(bars + 8 * islot, kUnit);
+            tc::mbar_arrive_expect_tx(bars + 8 * units.send, kUnit);
 #pragma unroll
             for (int hf = 0; hf < kHalves; ++hf)
-                tc::tma_load_2d(ring_at + islot * kUnit + hf * (kTile * 128), map, hf * 128, y, bars + 8 * islot);
+                tc::tma_load_2d(ring_at + units.send * kUnit + hf * (kTile * 128), map, hf * 128, y, bars + 8 * units.send);
         }
-        islot = islot + 1 == kUnits ? 0 : islot + 1;
+        units.sent();
         ++issued;
     };
     auto begin = [&]() {  // the stretch's first copies
@@ -321,17 +319,17 @@ __global__ void __launch_bounds__(kThreads, per_sm(D)) gdn_kv_attn_rows_kernel(c
         for (int e = 0; e < kHalves * 8; ++e) o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.0f;
 
         auto wait_unit = [&]() {
-            if (!tc::mbar_wait(bars + 8 * slot, parity, p.wait_ns)) {
+            if (units.gave_up) return;
+            if (!__all_sync(~0u, tc::mbar_wait(bars + 8 * units.slot, units.parity, p.wait_ns))) {
                 if (lane == 0) atomicOr(p.status, 1);
-                tc::mbar_wait(bars + 8 * slot, parity, kDrainNs);  // the copy lands before its place is used again
+                units.gave_up = true;
+                CopyRing<kUnits> left = units;  // what is in flight lands before the CTA ends
+                for (int i = units.pending(); i > 0; --i, left.read()) tc::mbar_wait(bars + 8 * left.slot, left.parity, kDrainNs);
             }
         };
         auto next_unit = [&]() {
             __syncwarp();
-            if (++slot == kUnits) {
-                slot = 0;
-                parity ^= 1;
-            }
+            units.read();
             issue();
         };
 
@@ -354,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(D)) gdn_kv_attn_rows_kernel(c
                     uint4 k[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        k[j] = *reinterpret_cast<const uint4*>(ring + slot * kUnit + hf * (kTile * 128) + (8 * j + g) * 128 + (((2 * q4 + cc) ^ g) << 4));
+                        k[j] = *reinterpret_cast<const uint4*>(ring + units.slot * kUnit + hf * (kTile * 128) + (8 * j + g) * 128 + (((2 * q4 + cc) ^ g) << 4));
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -431,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(D)) gdn_kv_attn_rows_kernel(c
                 uint4 v[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    v[k] = *reinterpret_cast<const uint4*>(ring + slot * kUnit + hf * (kTile * 128) + (8 * (k >> 1) + 2 * q4 + (k & 1)) * 128 +
+                    v[k] = *reinterpret_cast<const uint4*>(ring + units.slot * kUnit + hf * (kTile * 128) + (8 * (k >> 1) + 2 * q4 + (k & 1)) * 128 +
                                                            ((g ^ ((2 * q4 + (k & 1)) & 7)) << 4));
                 if (tail) {  // whatever lies past the end: zeros
 #pragma unroll
