@@ -196,6 +196,25 @@ __device__ __forceinline__ void split4_f16(float e0, float e1, float e2, float e
     lo = la | (lb << 16);
 }
 
+// Four softmax weights of a block, 0 <= w <= 256 and the block's largest above 2^7, as
+// e4m3 hi + 2^-5 lo: hi = RNE(w), within 2^3 of w, and lo = RNE(2^5 (w - hi)), 2^8 at
+// most.  Within 2^-8 of w (and f16's 2^-12) while w is above 2^-6, and within
+// 2^-15, which is 2^-22 of the block's largest, below.
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ void split4_weights(float e0, float e1, float e2, float e3, uint32_t& hi, uint32_t& lo) {
+    constexpr uint32_t k32 = 0x50005000u;  // 2^5, twice
+    const uint32_t a = f16x2(e0, e1), b = f16x2(e2, e3);
+    const uint32_t ha = e4m3x2_of_f16x2(a), hb = e4m3x2_of_f16x2(b);
+    const uint32_t la = e4m3x2_of_f16x2(mul_f16x2(sub_f16x2(a, f16x2_of_e4m3x2(ha)), k32));
+    const uint32_t lb = e4m3x2_of_f16x2(mul_f16x2(sub_f16x2(b, f16x2_of_e4m3x2(hb)), k32));
+    hi = ha | (hb << 16);
+    lo = la | (lb << 16);
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));

@@ -1,5 +1,5 @@
-// gdn_kv_tc.cuh -- tcgen05 wrappers for 8-bit operands (kind::f8f6f4) and wide
-// TMEM reads and writes, used by the tiled attention over the paged cache.
+// gdn_kv_tc.cuh -- tcgen05 wrappers for 8-bit operands (kind::f8f6f4, and
+// kind::mxf8f6f4 with block scales) and wide TMEM reads and writes, used by the tiled attention over the paged cache.
 #pragma once
 
 #include <stdint.h>
@@ -7,10 +7,9 @@
 namespace gdn {
 namespace tc {
 
-// Instruction descriptor, kind::f8f6f4: e4m3 A and B, fp32 D; A K-major, B
-// K-major or (b_mn) MN-major.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool b_mn) {
-    return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// Instruction descriptor, kind::f8f6f4: e4m3 A and B (K-major), fp32 D.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 // Shared-memory matrix descriptor of an MN-major operand of 8-bit elements with
@@ -36,14 +35,34 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint6
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
 }
 
-// The same with A in tensor memory: an M = 128 x K = 32 slice is 128 lanes x 8
-// columns, column c of a lane holding elements 4c .. 4c + 3 from the low byte up.
-__device__ __forceinline__ void mma_e4m3_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// Instruction descriptor, kind::mxf8f6f4: e4m3 A (K-major) and B (MN-major), fp32 D, and
+// for every K = 32 a power of two (ue8m0: the byte x stands for 2^(x - 127)) for each row of A and
+// column of B; A's is byte `a_byte` of its scale words, B's byte 0.
+__host__ __device__ constexpr uint32_t idesc_mx_e4m3(int M, int N, int a_byte) {
+    return (1u << 16) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24) | ((uint32_t)a_byte << 29);
+}
+
+// D (+)= (scaled A) (scaled B) for one K = 32 step, A in tensor memory: an M = 128 x
+// K = 32 slice is 128 lanes x 8 columns, column c of a lane holding elements 4c .. 4c + 3
+// from the low byte up.  The
+// scale words of rows 32 j + i of A (columns of B) are lane i, column j from
+// `a_scale` (`b_scale`), the same in all four lane quarters.
+__device__ __forceinline__ void mma_mx_e4m3_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t a_scale, uint32_t b_scale, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], [%1], %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate));
+}
+
+// 32 rows of 16 bytes from shared memory (one after another) to four columns of
+// lanes 0 to 31, and to the other three lane quarters: the layout of scale
+// words.  In order with this thread's later MMAs.
+__device__ __forceinline__ uint64_t smem_desc_rows16(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128u >> 4) << 32 | (uint64_t)1 << 46;
+}
+__device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t rows16) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(rows16) : "memory");
 }
 
 // 32 consecutive fp32 columns of this thread's TMEM lane, waited for.
@@ -61,26 +80,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
         : "memory");
 }
 
-// 64 consecutive fp32 columns of this thread's TMEM lane, waited for.
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
-        "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
-        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, "
-        "%51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
-          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
-          "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
-          "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]),
-          "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]),
-          "=f"(v[40]), "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]),
-          "=f"(v[48]), "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]),
-          "=f"(v[56]), "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63])
-        : "r"(taddr)
-        : "memory");
-}
-
 // 32 consecutive 32-bit columns of this thread's TMEM lane (tmem_wait_st() completes it).
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
     asm volatile(
@@ -91,16 +90,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) 
           "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]),
           "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]),
           "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
-        : "memory");
-}
-
-// 16 consecutive 32-bit columns of this thread's TMEM lane (tmem_wait_st() completes it).
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12,"
-        " %13, %14, %15, %16};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-          "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
 

@@ -4,10 +4,18 @@
 // a_j, b_j the scales of token j's blocks,
 //   t_j = scale log2(e) a_j (q . c_j) + log2 b_j,   o = sum 2^(t_j - m) w_j / sum 2^(t_j - m) / b_j.
 //
-// Both products take the cache's codes as they are (kind::f8f6f4): q and the
-// weights are split into two e4m3 numbers, hi + lo, and every contraction runs
-// over both, twice the products at twice bf16's rate, with half its bytes
-// of operands and no conversion of a tile.
+// Both products take the cache's codes as they are: q and the weights are split
+// into two e4m3 numbers, hi + lo, and every contraction runs over both, twice
+// the products at twice bf16's rate, with half its bytes of operands and no
+// conversion of a tile.
+//
+// The weights' product is the block-scaled kind (mxf8f6f4).  A row's weights of 32
+// tokens, which share a value scale b, are a block with a power of two of its own, 2^e with the
+// block's largest weight in (2^7, 2^8] 2^e, and lo's is 2^(e - 5): a weight is
+// within 2^-8 of itself, or within 2^-22 of its block's largest where it is below 2^-14 of that,
+// however far the block lies below the row's maximum.  (With one power
+// for a whole row the smallest step was 2^-14 of the row's maximum: a flat tail behind
+// one token with much of the softmax, or behind a page with a large value scale, was lost.)
 //
 // Roles of the CTA's 24 warps: one loads tiles (TMA) and their scales; one
 // issues the MMAs; sixteen are the softmax, in two teams that take turns at the
@@ -19,12 +27,13 @@
 // Tensor memory: tiles of logits (128 columns each: two for d = 256, three for
 // 128), over which their weights are written as the second product's A operand,
 // and the output (d columns).  The tensor pipe runs the logits of one or two
-// tiles ahead, then O += P V of the tile whose weights are ready.
+// tiles ahead, then O += P V of the tile whose weights are ready.  The exponents of a
+// tile's blocks go by way of shared memory, from where the product's issuer copies
+// them into columns of the logits that are free by then.
 //
 // The reference m of a row is raised, and the output rescaled in tensor
-// memory, only when a tile's maximum exceeds it by more than 2^3.8: weights
-// are held times 2^5, so they stay below e4m3's 448, and the smallest step of
-// lo is 2^-14 of a weight of 1.
+// memory, only when a tile's maximum exceeds it by more than 2^8: what
+// bounds that is fp32's range (sums of 2^8 times the scales' 2^-100 to 2^120), not the weights' format.
 //
 // The list of all (request, row tile, head, token tile) is cut evenly over
 // the CTAs, one to an SM, causal tiles that nobody sees left out; an item that
@@ -56,8 +65,9 @@ constexpr int kThreads = (kSoftWarps + 2 + kQWarps) * 32;
 constexpr int kTeamWarps = kSoftWarps / 2;
 constexpr int kM = 128;                 // rows of an item
 constexpr int kN = 128;                 // tokens of a tile
-constexpr float kPExp = 5.0f;           // weights are held times 2^5
-constexpr float kGrow = 3.8f;           // 2^(5 + 3.8) = 446
+constexpr float kGrow = 8.0f;           // how far a weight may exceed the reference, in powers of two
+constexpr float kBlockExp = 8.0f;       // a block's largest weight is held at most 2^8,
+constexpr int kLoExp = 5;               // and what is left of a weight times 2^5
 constexpr int kScaleRing = 8;
 constexpr int kSoftRegs = 88, kOtherRegs = 64;  // 512 x 88 + 256 x 64 = 768 x 80
 // An item's beginning and end, in tiles (the 8,192-token prompt took 606 us at 6, and 864,
@@ -76,16 +86,21 @@ struct TilesSmem {
     static constexpr bool kEarly = D == 256;                  // the product starts on half the weights
     alignas(1024) uint8_t q[kQBufs][2][kM * D];               // hi, lo
     alignas(1024) uint8_t ring[kSlots][kSlot];
-    float4 scales[kScaleRing][4];                             // of 32 tokens: key scale, log2 of the value scale, 1 / value scale
+    float2 scales[kScaleRing][4];                             // of 32 tokens: key scale, log2 of the value scale
     float rf[kQBufs][kM];
     float ref[2][2][kM];                                      // the rows' references after a team's tiles, two of them in turn
     float top[2][2][2][kM];                                   // by team and half: the rows' maxima of two tiles in turn
     float ml[2][2][kM], mr[2][2][2][kM];                      // by item: the teams' references; each half's sum
-    alignas(16) uint8_t stage[kSoftWarps][32 * 32];           // a warp's 32 rows x 16 columns of output on their way out
+    // exponents of a tile's blocks: for tokens 0 .. 31 of each half, and 32 .. 63, row 32 j + i's word
+    // at 16 i + 4 j, byte 2 half + part; and a page of exponents 0 for the values
+    alignas(128) uint8_t block_exp[kBufs][2][512], no_exp[512];
+    union {
+        alignas(16) uint8_t stage[kSoftWarps][32 * 32];       // a warp's 32 rows x 16 columns of output on their way out
+        int qbase[kThreads];                                  // (before the first item)
+    };
     alignas(8) uint64_t full[kSlots], empty[kSlots], s_full[kBufs], p_ready[2][kBufs], o_done[kBufs], scales_full[kScaleRing];
     uint64_t q_full[kQBufs], q_empty[kQBufs], item_done, o_free, drained;
     long long scan[kThreads / 32];
-    int qbase[kThreads];
     int at_b, at_t, at_h, at_v;
     uint32_t tmem;
     int dead;
@@ -167,7 +182,7 @@ struct RowMap {
 __device__ __forceinline__ float factor(float m, float top) { return m == top ? 1.0f : ex2(m - top); }
 
 __device__ __forceinline__ float lse_of(float m, float l) {
-    return l == 0.0f ? -INFINITY : ((m == -INFINITY ? 0.0f : m) - kPExp + log2f(l)) * 0.69314718055994531f;
+    return l == 0.0f ? -INFINITY : ((m == -INFINITY ? 0.0f : m) + log2f(l)) * 0.69314718055994531f;
 }
 
 template <int D>
@@ -290,6 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
         tc::mbar_init(item_done, 1);
         tc::mbar_init(drained, kTwo ? 2 : 1);
     }
+    if (tid < 128) reinterpret_cast<uint32_t*>(sm.no_exp)[tid] = 0x7f7f7f7fu;
+    tc::fence_async_smem();
     if (warp == kMmaWarp) tc::tmem_alloc(tc::smem_u32(&sm.tmem), 512);
     tc::fence_before_sync();
     __syncthreads();
@@ -408,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                     if (kv == 0) {
                         // the place in the ring is free: its last readers were done before the
                         // weights of the tile whose keys lay in this slot were
-                        if ((lane >> 2) == k) sm.scales[g % kScaleRing][lane & 3] = make_float4(ks, lv, ex2(-lv), 0.0f);
+                        if ((lane >> 2) == k) sm.scales[g % kScaleRing][lane & 3] = make_float2(ks, lv);
                         __syncwarp();
                         if (lane == 0) tc::mbar_arrive(scales_full + 8 * (g % kScaleRing));
                     }
@@ -445,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
         // d = 256, where the products take 1,024 each, one warp issues both, and the
         // tensor pipe's order keeps a tile's weights until their product has read
         // them; for d = 128 (512 each) a warp for each, the logits' one waiting for that product.
-        constexpr uint32_t id_s = tc::idesc_e4m3(kM, kN, false), id_o = tc::idesc_e4m3(kM, D, true);
+        constexpr uint32_t id_s = tc::idesc_e4m3(kM, kN);
         const uint32_t ring = tc::smem_u32(sm.ring[0]);
         auto logits = [&](int g, int qb, bool last) {
             const int u = 2 * g, slot = u % kSlots, buf = g % kBufs;
@@ -474,6 +491,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
             wait(full + 8 * slot, u / kSlots);
             const uint64_t v = tc::smem_desc_mn_sw128(ring + slot * kSlot, kHalfBytes);
             const uint32_t a = tmem + buf * kN;
+            // the exponents: columns 16 .. 31 of the logits, whose readers were done before the weights were
+            const uint32_t exps = a + 16, no_exps = exps + 8;
+            const uint64_t from = tc::smem_desc_rows16(tc::smem_u32(sm.block_exp[buf][0])), none = tc::smem_desc_rows16(tc::smem_u32(sm.no_exp));
             // kEarly: the weights come in two halves, of tokens 0 .. 31 and 64 .. 95 first, and the
             // product of those runs while the others' exponentials do (d = 256: 529 -> 511 us for 1,024
             // queries after 30,000 tokens; d = 128, where the softmax is the longer, 369 -> 388 us)
@@ -484,11 +504,16 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                     tc::fence_after_sync();
                 }
                 if (tc::elect_one()) {
+                    if (c == 0)
+#pragma unroll
+                        for (int n = 0; n < kHalves; ++n) tc::copy_scales(no_exps + 4 * n, none);
+                    tc::copy_scales(exps + 4 * c, from + (c * 512 >> 4));
 #pragma unroll
                     for (int half = 0; half < 2; ++half)
 #pragma unroll
                         for (int part = 0; part < 2; ++part)
-                            tc::mma_e4m3_ts(tO, a + half * 64 + c * 8 + part * 16, v + ((2 * half + c) * 32 * 128 >> 4), id_o, c + half + part > 0 || !first);
+                            tc::mma_mx_e4m3_ts(tO, a + half * 64 + c * 32 + part * 8, v + ((2 * half + c) * 32 * 128 >> 4),
+                                               tc::idesc_mx_e4m3(kM, D, 2 * half + part), exps + 4 * c, no_exps, c + half + part > 0 || !first);
                 }
                 __syncwarp();
             }
@@ -579,8 +604,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
     } else {
         // ----------------------------------------------------------- softmax
         // Team 0 has the even tiles of the CTA, team 1 the odd ones, a thread half a
-        // row: 64 tokens.  A half's weights replace the first 32 columns of its own
-        // logits (hi of its 64 tokens, then lo).
+        // row: 64 tokens, two blocks.  A block's weights replace the first 16 columns of its own
+        // logits (hi, then lo).
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         const int quad = warp & 3, half = (warp >> 2) & 1, team = warp >> 3, local = quad * 32 + lane;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16, tH = tmem + lanes + half * 64;
@@ -619,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                 const int buf = g % kBufs;
                 const uint32_t tS = tH + buf * kN;
                 wait(scales_full + 8 * (g % kScaleRing), g / kScaleRing);
-                const float4 sc0 = sm.scales[g % kScaleRing][2 * half], sc1 = sm.scales[g % kScaleRing][2 * half + 1];
+                const float2 sc0 = sm.scales[g % kScaleRing][2 * half], sc1 = sm.scales[g % kScaleRing][2 * half + 1];
                 const float f0 = rf * sc0.x, f1 = rf * sc1.x;
                 // the thread's 64 tokens as bits: those below its limit, or below the tree and the nodes it sees
                 const bool masked = j * kN + kN > all_see;
@@ -639,8 +664,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                 wait(s_full + 8 * buf, g / kBufs);
                 tc::fence_after_sync();
 
-                // ---- the tile's maximum
-                float top = -INFINITY;
+                // ---- the blocks' maxima and the tile's
+                float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll 1
                 for (int c = 0; c < 2; ++c) {
                     float s[32];
@@ -658,8 +683,11 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
 #pragma unroll
                     for (int k = 0; k < 4; ++k) t4[k] = fmaxf(fmaxf(t4[k], s[8 * k + 5]), fmaxf(s[8 * k + 6], s[8 * k + 7]));
                     const float t = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-                    top = fmaxf(top, fmaf(t, c ? f1 : f0, c ? sc1.y : sc0.y));
+                    const float u = fmaf(t, c ? f1 : f0, c ? sc1.y : sc0.y);
+                    if (c) top1 = u;
+                    else top0 = u;
                 }
+                float top = fmaxf(top0, top1);
                 sm.top[(g >> 1) & 1][team][half][local] = top;
                 tc::named_sync(my_bar, 96);
 
@@ -704,12 +732,16 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                     tc::fence_async_smem();
                 }
                 // ---- weights
-                const float shift = kPExp - (m == -INFINITY ? 0.0f : m);
+                const float ref0 = m == -INFINITY ? 0.0f : m;
 #pragma unroll 1
                 for (int c = 0; c < 2; ++c) {
                     float s[32];
                     tc::tmem_ld32(tS + c * 32, s);
-                    const float f = c ? f1 : f0, a = (c ? sc1.y : sc0.y) + shift;
+                    // the block's exponent; far below the reference it stops where its byte does, and
+                    // the weights fade (a block that is not seen is there too)
+                    const float lv = c ? sc1.y : sc0.y;
+                    const float e = fminf(fmaxf(ceilf((c ? top1 : top0) - ref0), -110.0f), 100.0f) - kBlockExp;
+                    const float f = c ? f1 : f0, a = lv - ref0 - e;
                     float part[2] = {0.0f, 0.0f};
                     uint32_t hi[8], lo[8];
                     if (!masked) {
@@ -719,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                                         e3 = ex2(fmaf(s[4 * k + 3], f, a));
                             part[0] += e0 + e1;
                             part[1] += e2 + e3;
-                            split4_f16(e0, e1, e2, e3, hi[k], lo[k]);
+                            split4_weights(e0, e1, e2, e3, hi[k], lo[k]);
                         }
                     } else {
                         const uint32_t bits = c ? vis[1] : vis[0];
@@ -730,15 +762,18 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
                             for (int i = 0; i < 4; ++i) e[i] = (bits >> (4 * k + i)) & 1 ? ex2(fmaf(s[4 * k + i], f, a)) : 0.0f;
                             part[0] += e[0] + e[1];
                             part[1] += e[2] + e[3];
-                            split4_f16(e[0], e[1], e[2], e[3], hi[k], lo[k]);
+                            split4_weights(e[0], e[1], e[2], e[3], hi[k], lo[k]);
                         }
                     }
-                    tc::tmem_st8(tS + c * 8, hi);
-                    tc::tmem_st8(tS + 16 + c * 8, lo);
+                    tc::tmem_st8(tS + c * 32, hi);
+                    tc::tmem_st8(tS + c * 32 + 8, lo);
+                    const int x = 127 + (int)e;
+                    *reinterpret_cast<uint16_t*>(&sm.block_exp[buf][c][16 * lane + 4 * quad + 2 * half]) = (uint16_t)(x | (x - kLoExp) << 8);
                     // a row that sees nothing here takes nothing from the block's scale
                     const float sum = part[0] + part[1];
-                    if (sum != 0.0f) l = fmaf(sum, c ? sc1.z : sc0.z, l);
+                    if (sum != 0.0f) l = fmaf(sum, ex2(e - lv), l);
                     if (kEarly || c == 1) {
+                        tc::fence_async_smem();
                         tc::tmem_wait_st();
                         tc::fence_before_sync();
                         __syncwarp();

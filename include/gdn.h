@@ -739,9 +739,13 @@ size_t gdn_kv_attention_workspace_bytes(const gdn_kv_shape* shape);
  *          Its int32 at offset 0 is set non-zero if a bounded device wait
  *          gave up, and stays so; gdn_kv_attention_status() reads it.
  * Products are exact in the codes, sums are fp32.  q, times a power of two for
- * each row, is exact while within 2^-10 of the row's largest; a softmax weight
- * is within 2^-8 of itself (two e4m3 numbers), or 2^-11 (f16).  What lies in
- * the cache past a request's length is never used, whatever its bits.
+ * each row, is exact while within 2^-10 of the row's largest.  A softmax weight,
+ * times its block's value scale, is held
+ *   by the kernel of 128 rows as two e4m3 numbers with a power of two for every row and 32
+ *   tokens (position / 32): within 2^-8 of itself, or 2^-22 of the largest of those 32;
+ *   by the kernel of eight rows in f16: within 2^-11 of itself, or 2^-33 of the row's largest.
+ * So a long flat tail is kept however much of the softmax another token has.
+ * What lies in the cache past a request's length is never used, whatever its bits.
  * The sizes (T, the shape, and its width as the bound of the lengths) pick the
  * kernel, eight rows (queries x heads of a group) at a time or 128; the two
  * differ in last bits.  Up to eight rows a request, T * Hq / Hkv <= 8 * B, it is the

@@ -1,0 +1,164 @@
+"""Attention over the paged 8-bit cache where one token holds much of the softmax, or one
+page has a much larger value scale, before a long flat tail: the tail's weights are small
+beside the row's largest one, and together they are much of the output.
+
+The bound on the output has no term that grows with the number of visible tokens but that
+of fp32 sums (o: output, w_j: weights, sum 1, v_j: values, size = sum_j w_j |v_j|):
+  - one rounding to bf16, 2^-8 |o|;
+  - a weight held as two e4m3 numbers, 2^-4 * 2^-4 of itself, by way of f16, 2^-12 (in f16
+    alone: 2^-11): (2^-8 + 2^-12) size;
+  - below their normal ranges, per weight: the two numbers 2^-22 of the largest weight of the same 32
+    tokens, in powers of two with the value scale taken in (a block of 32 is held within
+    (2^7, 2^8], the second number's smallest step is 2^-9 * 2^-5, half of it counts);
+  - a logit's error ds in powers of two moves the output by 2 ln 2 ds size: q as hi + lo, 2^-17 max|q|
+    an element; fp32 sums of d products; ex2 and the fused steps;
+  - sums over the tokens, sixteen at least to a step: L / 16 * 2^-23, doubled."""
+import math
+
+import pytest
+import torch
+
+from hybrid_linear_attention_conv_gb300 import gdn
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+PAGE = 64
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from hybrid_linear_attention_conv_gb300 import build
+    build.build()
+    gdn.load()
+    assert torch.cuda.is_available()
+
+
+def nearest(x):
+    return x.clamp(-448, 448).to(torch.float8_e4m3fn)
+
+
+class Tail:
+    """One request of L tokens, `new` of them queries, one key/value head; logits of all but
+    token `at` are of order one."""
+
+    def __init__(self, L, new, G, d, seed):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        self.L, self.n, self.G, self.d = L, new, G, d
+        pages = -(-L // PAGE)
+        self.order = torch.randperm(pages, generator=g, device=DEV)
+        k = torch.randn((pages * PAGE, d), generator=g, device=DEV) * 100
+        k[:, 0] = 0
+        v = torch.randn(d, generator=g, device=DEV) * 60 + torch.randn((pages * PAGE, d), generator=g, device=DEV) * 30
+        self.k, self.v = nearest(k), nearest(v)
+        self.ks = torch.full((pages,), 2.0 ** -7, device=DEV)
+        self.vs = torch.full((pages,), 2.0 ** -6, device=DEV)
+        self.q = torch.randn((new, G, d), generator=g, device=DEV).to(torch.bfloat16)
+        self.q[..., 0] = 1.0
+
+    def lift(self, at, bits):
+        """Token `at`'s logits `bits` powers of two above (or below) what they are."""
+        want = bits / (d_scale(self.d) * float(self.ks[at // PAGE]) * 448.0)
+        self.k[at, 0] = math.copysign(448.0, want)
+        self.q[..., 0] = abs(want)
+
+    def share(self, at, part):
+        """Token `at` with about that part of the last row's softmax."""
+        others = torch.logsumexp(self.logits().masked_fill(torch.arange(self.L, device=DEV) == at, -math.inf)[-1, 0], 0) / math.log(2)
+        self.lift(at, float(others) + math.log2(part / (1 - part)) - float(self.logits()[-1, 0, at]) / math.log(2))
+
+    def logits(self):
+        k = self.k.double() * self.ks.double().repeat_interleave(PAGE)[:, None]
+        return torch.einsum("ngd,ld->ngl", self.q.double(), k[:self.L]) * self.d ** -0.5
+
+    def run(self, tiles):
+        d, pages = self.d, self.ks.numel()
+        codes = [torch.empty((pages, 1, PAGE, d), dtype=torch.float8_e4m3fn, device=DEV) for _ in range(2)]
+        scales = [torch.empty((pages, 1), device=DEV) for _ in range(2)]
+        for c, s, x, y in zip(codes, scales, (self.k, self.v), (self.ks, self.vs)):
+            c.view(torch.uint8)[self.order, 0] = x.view(torch.uint8).view(pages, PAGE, d)
+            s[self.order, 0] = y
+        # the kernel follows from the rows and the table's width: rows that no request has, and entries that none holds
+        pad, width = (9, pages + ((1 << 22) + 8192) // PAGE) if tiles else (0, pages)
+        table = torch.full((1, width), -1, dtype=torch.int32, device=DEV)
+        table[0, :pages] = self.order
+        q = torch.cat([self.q, self.q.new_zeros((pad, self.G, d))])
+        i32 = dict(dtype=torch.int32, device=DEV)
+        lse = torch.empty(q.shape[:2], device=DEV)
+        out = gdn.kv_attention(q, *codes, *scales, table, torch.tensor([0, self.n], **i32), torch.tensor([self.L], **i32), lse=lse)
+        return out[:self.n].double(), lse[:self.n].double()
+
+    def check(self, tiles):
+        out, lse = self.run(tiles)
+        L, d = self.L, self.d
+        a, b = (s.double().repeat_interleave(PAGE)[:L] for s in (self.ks, self.vs))
+        k, v = self.k.double()[:L], self.v.double()[:L]
+        raw = torch.einsum("ngd,ld->ngl", self.q.double(), k) * a
+        seen = torch.arange(L, device=DEV)[None] <= torch.arange(L - self.n, L, device=DEV)[:, None]
+        s = (raw * d_scale(d)).masked_fill(~seen[:, None], -math.inf)
+        m = s.amax(-1, keepdim=True)
+        w = torch.exp2(s - m)
+        total = w.sum(-1, keepdim=True)
+        w = w / total * b                                       # per code
+        o, size = w @ v, w @ v.abs()
+        blocks = torch.nn.functional.pad(w, (0, -L % 32)).unflatten(-1, (-1, 32))
+        top = blocks.amax(-1, keepdim=True).expand_as(blocks).flatten(-2)[..., :L] * seen[:, None]
+        q = self.q.double()
+        ds = d_scale(d) * a * (q.abs().amax(-1, keepdim=True) * 2.0 ** -17 * k.abs().sum(-1) + d * 2.0 ** -23 * (q.abs() @ k.abs().T))
+        ds = (ds + 2.0 ** -21 + (s + b.log2()).abs() * 2.0 ** -22).masked_fill(~seen[:, None], 0)
+        moved = 2 * math.log(2) * ds.amax(-1, keepdim=True)
+        sums = L / 16 * 2.0 ** -22
+        bound = 2.0 ** -8 * o.abs() + (2.0 ** -8 + 2.0 ** -12 + moved + sums) * size + 2.0 ** -22 * (top @ v.abs())
+        err = (out - o).abs()
+        assert torch.isfinite(out).all()
+        worst = float((err / bound).max())
+        norm = float((err.norm(dim=-1) / (o.norm(dim=-1) + size.norm(dim=-1))).max())
+        want = ((m + total.log2()) * math.log(2))[..., 0]
+        lse_err = float(((lse - want).abs() / (moved[..., 0] + sums + want.abs() * 2.0 ** -22 + 2.0 ** -20)).max())
+        print(f"L {L} d {d} tiles {tiles}: {worst:.3f} of the bound, {norm:.2e} of |o| + |size|, lse {lse_err:.3f}")
+        assert worst <= 1 and lse_err <= 1
+        # and as a whole: two roundings of 2^-8 to nearest, and the logits' part
+        assert norm <= 2.0 ** -8 + float(moved.max()) + sums
+
+
+def d_scale(d):
+    return d ** -0.5 * math.log2(math.e)
+
+
+FORMS = [(1, 6, 256), (130, 3, 256), (1, 8, 128), (130, 4, 128)]  # queries, rows a query, head size
+
+
+@pytest.mark.parametrize("tiles", [False, True])
+@pytest.mark.parametrize("new,G,d", FORMS)
+@pytest.mark.parametrize("L,part", [(2048, 0.5), (2048, 0.95), (8192, 0.8), (8192, 0.9), (32768, 0.5), (32768, 0.95)])
+def test_one_token_holds_much_of_the_softmax(L, part, new, G, d, tiles):
+    t = Tail(L, new, G, d, seed=L)
+    t.v[0] = nearest(t.v[0].float() * 0.01)  # a sink: its own value is small
+    t.share(0, part)
+    t.check(tiles)
+
+
+@pytest.mark.parametrize("tiles", [False, True])
+@pytest.mark.parametrize("new,G,d", FORMS)
+@pytest.mark.parametrize("L,at,bits", [(8192, 0, 10), (8192, 0, 14), (8192, 4099, 16), (8192, 0, 18), (8192, 5, 20), (30000, 0, 18),
+                                       (30000, 29000, 16), (700, 0, 17)])
+def test_a_token_without_value_far_above_the_rest(L, at, bits, new, G, d, tiles):
+    t = Tail(L, new, G, d, seed=L + bits)
+    t.v[at] = 0
+    t.lift(at, bits)
+    t.check(tiles)
+
+
+@pytest.mark.parametrize("tiles", [False, True])
+@pytest.mark.parametrize("new,G,d", FORMS)
+@pytest.mark.parametrize("bits", [8, 12, 14, 20])
+def test_one_page_with_a_much_larger_value_scale(bits, new, G, d, tiles):
+    """The page's scale comes from one token that is hardly attended to; its other tokens'
+    codes are what is left of ordinary values."""
+    L, page, at = 4096, 17, 17 * PAGE + 40
+    t = Tail(L, new, G, d, seed=bits)
+    t.vs[page] = 2.0 ** (bits - 6)
+    rows = slice(page * PAGE, (page + 1) * PAGE)
+    t.v[rows] = nearest(t.v[rows].float() * 2.0 ** -bits)
+    t.v[at] = nearest(torch.randn(d, device=DEV) * 100)
+    t.lift(at, -bits - 8.0)
+    t.check(tiles)
