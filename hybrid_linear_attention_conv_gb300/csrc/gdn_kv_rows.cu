@@ -14,7 +14,8 @@
 // mma.sync.m16n8k16 with the codes, converted exactly to f16, as the 16-row
 // operand, and the eight rows as the n = 8 one, so no part of a tile is empty:
 //   S^T [tokens x rows] = K Q^T,     O^T [columns x rows] += V^T P^T.
-// q (bf16, times a power of two) is exact in f16, a weight is rounded by 2^-11.
+// q (bf16, times a power of two) is exact in f16, a weight, held times 2^15, is within
+// 2^-11 of itself, or 2^-40 of the row's largest.
 // (mma.sync on e4m3 operands is no shorter way: it took 870 instructions for a tile of
 // 32 tokens x 128, with q and the weights as two e4m3 numbers each.  tcgen05's
 // tiles of 128 rows would be fifteen sixteenths empty here.)
@@ -64,7 +65,7 @@ constexpr int kRows = 8;
 // columns a thread needs more than the 168 registers that twelve warps leave it.
 __host__ __device__ constexpr int per_sm(int d) { return d == 256 ? 2 : 3; }
 __host__ __device__ constexpr int ring_bytes(int d) { return d == 256 ? 24 * 1024 : 16 * 1024; }
-constexpr float kPScale = 8.0f;         // weights are held times 2^8
+constexpr float kPScale = 15.0f;        // weights, at most 1, are held times 2^15: f16's largest binade
 constexpr uint64_t kDrainNs = 200000000ull;
 // An item's beginning and end, in tiles.  251 requests of up to 3,000 tokens, 32/8
 // heads of 128: 162 us without, 146 with 4, 132 with 8 and 16; 64 long ones of 256 172,

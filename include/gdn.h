@@ -743,7 +743,7 @@ size_t gdn_kv_attention_workspace_bytes(const gdn_kv_shape* shape);
  * times its block's value scale, is held
  *   by the kernel of 128 rows as two e4m3 numbers with a power of two for every row and 32
  *   tokens (position / 32): within 2^-8 of itself, or 2^-22 of the largest of those 32;
- *   by the kernel of eight rows in f16: within 2^-11 of itself, or 2^-33 of the row's largest.
+ *   by the kernel of eight rows in f16: within 2^-11 of itself, or 2^-40 of the row's largest.
  * So a long flat tail is kept however much of the softmax another token has.
  * What lies in the cache past a request's length is never used, whatever its bits.
  * The sizes (T, the shape, and its width as the bound of the lengths) pick the

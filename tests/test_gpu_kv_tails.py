@@ -10,6 +10,8 @@ of fp32 sums (o: output, w_j: weights, sum 1, v_j: values, size = sum_j w_j |v_j
   - below their normal ranges, per weight: the two numbers 2^-22 of the largest weight of the same 32
     tokens, in powers of two with the value scale taken in (a block of 32 is held within
     (2^7, 2^8], the second number's smallest step is 2^-9 * 2^-5, half of it counts);
+    (the kernel of eight rows at a time, in f16 times 2^15: 2^-11 size, and 2^-25 * 2^-15 of the row's largest;
+    q there is f16 too, at least 224 at its largest: 2^-32 max|q|);
   - a logit's error ds in powers of two moves the output by 2 ln 2 ds size: q as hi + lo, 2^-17 max|q|
     an element; fp32 sums of d products; ex2 and the fused steps;
   - sums over the tokens, sixteen at least to a step: L / 16 * 2^-23, doubled."""
@@ -70,7 +72,8 @@ class Tail:
         k = self.k.double() * self.ks.double().repeat_interleave(PAGE)[:, None]
         return torch.einsum("ngd,ld->ngl", self.q.double(), k[:self.L]) * self.d ** -0.5
 
-    def run(self, tiles):
+    def run(self, tiles, copies=1):
+        """copies: that many requests alike, over the same pages; the last one's rows are returned."""
         d, pages = self.d, self.ks.numel()
         codes = [torch.empty((pages, 1, PAGE, d), dtype=torch.float8_e4m3fn, device=DEV) for _ in range(2)]
         scales = [torch.empty((pages, 1), device=DEV) for _ in range(2)]
@@ -79,16 +82,18 @@ class Tail:
             s[self.order, 0] = y
         # the kernel follows from the rows and the table's width: rows that no request has, and entries that none holds
         pad, width = (9, pages + ((1 << 22) + 8192) // PAGE) if tiles else (0, pages)
-        table = torch.full((1, width), -1, dtype=torch.int32, device=DEV)
-        table[0, :pages] = self.order
-        q = torch.cat([self.q, self.q.new_zeros((pad, self.G, d))])
+        table = torch.full((copies, width), -1, dtype=torch.int32, device=DEV)
+        table[:, :pages] = self.order
+        q = torch.cat([self.q.repeat(copies, 1, 1), self.q.new_zeros((pad, self.G, d))])
         i32 = dict(dtype=torch.int32, device=DEV)
         lse = torch.empty(q.shape[:2], device=DEV)
-        out = gdn.kv_attention(q, *codes, *scales, table, torch.tensor([0, self.n], **i32), torch.tensor([self.L], **i32), lse=lse)
-        return out[:self.n].double(), lse[:self.n].double()
+        out = gdn.kv_attention(q, *codes, *scales, table, torch.arange(copies + 1, **i32) * self.n, torch.full((copies,), self.L, **i32), lse=lse)
+        last = slice((copies - 1) * self.n, copies * self.n)
+        return out[last].double(), lse[last].double()
 
-    def check(self, tiles):
-        out, lse = self.run(tiles)
+    def check(self, tiles, f16=False, copies=1):
+        """f16: the bound of the kernel of eight rows at a time."""
+        out, lse = self.run(tiles, copies)
         L, d = self.L, self.d
         a, b = (s.double().repeat_interleave(PAGE)[:L] for s in (self.ks, self.vs))
         k, v = self.k.double()[:L], self.v.double()[:L]
@@ -103,11 +108,14 @@ class Tail:
         blocks = torch.nn.functional.pad(w, (0, -L % 32)).unflatten(-1, (-1, 32))
         top = blocks.amax(-1, keepdim=True).expand_as(blocks).flatten(-2)[..., :L] * seen[:, None]
         q = self.q.double()
-        ds = d_scale(d) * a * (q.abs().amax(-1, keepdim=True) * 2.0 ** -17 * k.abs().sum(-1) + d * 2.0 ** -23 * (q.abs() @ k.abs().T))
+        ds = d_scale(d) * a * (q.abs().amax(-1, keepdim=True) * 2.0 ** (-32 if f16 else -17) * k.abs().sum(-1) + d * 2.0 ** -23 * (q.abs() @ k.abs().T))
         ds = (ds + 2.0 ** -21 + (s + b.log2()).abs() * 2.0 ** -22).masked_fill(~seen[:, None], 0)
         moved = 2 * math.log(2) * ds.amax(-1, keepdim=True)
         sums = L / 16 * 2.0 ** -22
-        bound = 2.0 ** -8 * o.abs() + (2.0 ** -8 + 2.0 ** -12 + moved + sums) * size + 2.0 ** -22 * (top @ v.abs())
+        if f16:
+            top = w.amax(-1, keepdim=True) * seen[:, None]
+        held, below = (2.0 ** -11, 2.0 ** -40) if f16 else (2.0 ** -8 + 2.0 ** -12, 2.0 ** -22)
+        bound = 2.0 ** -8 * o.abs() + (held + moved + sums) * size + below * (top @ v.abs())
         err = (out - o).abs()
         assert torch.isfinite(out).all()
         worst = float((err / bound).max())
@@ -162,3 +170,14 @@ def test_one_page_with_a_much_larger_value_scale(bits, new, G, d, tiles):
     t.v[at] = nearest(torch.randn(d, device=DEV) * 100)
     t.lift(at, -bits - 8.0)
     t.check(tiles)
+
+
+@pytest.mark.parametrize("G,d", [(6, 256), (8, 128)])
+@pytest.mark.parametrize("bits", [24, 30, 34, 36])
+def test_eight_rows_keep_a_tail_far_below(bits, G, d):
+    """One token a request, which is the kernel of eight rows whatever the table's width; so many
+    requests that one is not spread over CTAs, whose parts have maxima of their own."""
+    t = Tail(4096, 1, G, d, seed=bits)
+    t.v[0] = 0
+    t.lift(0, bits)
+    t.check(False, f16=True, copies=1000)
