@@ -397,6 +397,21 @@ PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
     return fn;
 }
 
+// The device's give-up word, which every attention call on it reports to.
+__device__ int g_kv_gave_up = 0;
+
+cudaError_t gave_up_word(int** word) {  // its address on the current device, looked up once
+    static std::once_flag once[64];
+    static cudaError_t err[64];
+    static void* at[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= 64) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+    std::call_once(once[dev], [dev] { err[dev] = cudaGetSymbolAddress(&at[dev], g_kv_gave_up); });
+    *word = static_cast<int*>(at[dev]);
+    return err[dev];
+}
+
 // A cache as rows of d codes, loaded in boxes of `rows` rows x 128 bytes with the
 // 128-byte swizzle (16-byte chunk c of row r lies at c ^ (r & 7)).
 bool encode_cache_map(CUtensorMap* map, const uint8_t* cache, const gdn_kv_shape* s, int rows) {
@@ -602,6 +617,8 @@ int gdn_kv_attention(const gdn_kv_shape* shape, int32_t T, const gdn_bf16* q, in
     p.tree = tree;
     p.out = out;
     p.lse = lse;
+    cudaError_t e = gave_up_word(&p.gave_up);
+    if (e != cudaSuccess) return cuda_error(e, "looking up the attention's give-up word");
     p.status = reinterpret_cast<int*>(ws);
     p.spans = reinterpret_cast<int*>(ws + kKvSpansAt);
     p.span_rows = reinterpret_cast<int64_t*>(ws + kKvSpanRowsAt);
@@ -619,7 +636,7 @@ int gdn_kv_attention(const gdn_kv_shape* shape, int32_t T, const gdn_bf16* q, in
     p.scale_log2 = scale * 1.4426950408889634f;
     p.group_magic = ((1u << 22) + p.G - 1) / p.G;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = tiles ? launch_kv_attn_tiles(p, shape->d, st) : launch_kv_attn_rows(p, shape->d, st);
+    e = tiles ? launch_kv_attn_tiles(p, shape->d, st) : launch_kv_attn_rows(p, shape->d, st);
     return e == cudaSuccess ? GDN_OK : cuda_error(e, "cache attention launch");
 }
 
@@ -632,6 +649,21 @@ int gdn_kv_attention_status(const void* workspace, void* stream, int32_t* status
     if (e != cudaSuccess) return cuda_error(e, "reading the attention's status word");
     if (status != nullptr) *status = word;
     if (word != 0) return report_error(GDN_ERR_TIMEOUT, "a bounded device wait of an attention call gave up (status %d)", word);
+    return GDN_OK;
+}
+
+int gdn_kv_attention_device_status(void* stream, int32_t* status) {
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int* word = nullptr;
+    int32_t value = 0;
+    cudaError_t e = gave_up_word(&word);
+    if (e == cudaSuccess) e = cudaMemcpyAsync(&value, word, sizeof value, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e == cudaSuccess && value != 0) e = cudaMemsetAsync(word, 0, sizeof value, st);
+    if (e != cudaSuccess) return cuda_error(e, "reading the attention's give-up word");
+    if (status != nullptr) *status = value;
+    if (value != 0)
+        return report_error(GDN_ERR_TIMEOUT, "a bounded device wait of an attention call gave up (status %d)", value);
     return GDN_OK;
 }
 

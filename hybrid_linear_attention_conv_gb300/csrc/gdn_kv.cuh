@@ -97,6 +97,7 @@ struct KvAttnParams {
     const int64_t* tree;        // [T] or nullptr
     uint16_t* out;              // bf16 [T, Hq, d]
     float* lse;                 // [T, Hq] or nullptr
+    int* gave_up;               // the device's word: calls without a workspace of the caller's
     int* status;                // workspace: the status word,
     int* spans;                 // how many CTAs further the item goes that begins in a CTA,
     int64_t* span_rows;         // its eight rows' places in out (-1: none), or {first row of q, queries, row tile, head},
@@ -124,6 +125,12 @@ cudaError_t launch_kv_attn_tiles(KvAttnParams& p, int d, cudaStream_t s);
 size_t kv_attn_tiles_workspace(int d);
 
 #ifdef __CUDACC__
+// A bounded wait gave up.
+__device__ __forceinline__ void report_give_up(const KvAttnParams& p, int bit) {
+    atomicOr(p.status, bit);
+    atomicOr(p.gave_up, bit);
+}
+
 // Every kernel of a step is launched as a programmatic dependent of the one
 // before it on the stream: its blocks may be placed while that one drains, and
 // touch no memory that it may write before tc::grid_wait().

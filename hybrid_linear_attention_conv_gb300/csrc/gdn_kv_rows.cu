@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, per_sm(D)) gdn_kv_attn_rows_kernel(c
         auto wait_unit = [&]() {
             if (units.gave_up) return;
             if (!__all_sync(~0u, tc::mbar_wait(bars + 8 * units.slot, units.parity, p.wait_ns))) {
-                if (lane == 0) atomicOr(p.status, 1);
+                if (lane == 0) report_give_up(p, 1);
                 units.gave_up = true;
                 CopyRing<kUnits> left = units;  // what is in flight lands before the CTA ends
                 for (int i = units.pending(); i > 0; --i, left.read()) tc::mbar_wait(bars + 8 * left.slot, left.parity, kDrainNs);

@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
         if (*dead) return;
         if (!tc::mbar_wait(bar, parity, p.wait_ns)) {
             *dead = 1;
-            atomicOr(p.status, 2);
+            report_give_up(p, 2);
         }
     };
 

@@ -79,6 +79,7 @@ EXPORTS = [
     "gdn_kv_attention_workspace_bytes",
     "gdn_kv_attention",
     "gdn_kv_attention_status",
+    "gdn_kv_attention_device_status",
 ]
 
 
@@ -158,6 +159,7 @@ def load(path: str = LIB_PATH):
             "gdn_kv_attention_workspace_bytes": (SZ, [KV]),
             "gdn_kv_attention": (ctypes.c_int, [KV, I32, P, I64, P, P, P, P, P, P, P, P, F, P, P, P, SZ, P]),
             "gdn_kv_attention_status": (ctypes.c_int, [P, P, ctypes.POINTER(I32)]),
+            "gdn_kv_attention_device_status": (ctypes.c_int, [P, ctypes.POINTER(I32)]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -866,7 +868,7 @@ def kv_attention(q, k_cache, v_cache, k_scale, v_scale, table, start, lens, scal
     [B,width], start int32 [B+1] and lens int32 [B] as kv_plan leaves them; scale defaults to
     d^-0.5; tree int64 [T]: the draft nodes that a query sees, as bits (causal without it);
     lse fp32 [T,Hq], filled if given; workspace uint8, zeroed before its first use (by default
-    a new one)."""
+    a new one, of whose calls kv_attention_status() without a workspace tells)."""
     cache = _kv_cache(k_cache, v_cache, k_scale, v_scale)
     pages, Hkv, page, d = k_cache.shape
     qp, ldq = _rows3(q, "q")
@@ -878,7 +880,8 @@ def kv_attention(q, k_cache, v_cache, k_scale, v_scale, table, start, lens, scal
         out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=q.device)
     sh = _kv_shape(B, Hq, Hkv, d, page, pages, width)
     if workspace is None:
-        workspace = torch.zeros(max(int(load().gdn_kv_attention_workspace_bytes(sh)), 1), dtype=torch.uint8, device=q.device)
+        # its status word is not read (the device's is), and the kernels write the rest before they read it
+        workspace = torch.empty(max(int(load().gdn_kv_attention_workspace_bytes(sh)), 1), dtype=torch.uint8, device=q.device)
     i32, size = torch.int32, workspace.numel()
     rc = load().gdn_kv_attention(sh, T, qp, ldq, *cache, _ptr(table, i32, "table", (B, width)), _ptr(start, i32, "start", (B + 1,)),
                                  _ptr(lens, i32, "lens", (B,)), _ptr(tree, torch.int64, "tree", (T,)),
@@ -890,10 +893,16 @@ def kv_attention(q, k_cache, v_cache, k_scale, v_scale, table, start, lens, scal
     return out
 
 
-def kv_attention_status(workspace: torch.Tensor) -> int:
+def kv_attention_status(workspace: torch.Tensor | None = None) -> int:
     """Synchronise the current stream and return the status word of the attention calls that
-    used `workspace` (0: their results are valid; non-zero: a bounded device wait gave up)."""
+    used `workspace`, or without one of all on the current device since the last such reading
+    (0: their results are valid; non-zero: a bounded device wait gave up)."""
     st = ctypes.c_int32(0)
+    if workspace is None:
+        rc = load().gdn_kv_attention_device_status(_stream(), ctypes.byref(st))
+        if rc not in (0, -8):
+            _check(rc, "gdn_kv_attention_device_status")
+        return int(st.value)
     rc = load().gdn_kv_attention_status(_dev(workspace, torch.uint8, "workspace"), _stream(), ctypes.byref(st))
     if rc not in (0, -8):
         _check(rc, "gdn_kv_attention_status")

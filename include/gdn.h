@@ -737,7 +737,8 @@ size_t gdn_kv_attention_workspace_bytes(const gdn_kv_shape* shape);
  *          zeroed by the caller before its first use; a call leaves it as the
  *          next one needs it.  Calls that may overlap need workspaces of their own.
  *          Its int32 at offset 0 is set non-zero if a bounded device wait
- *          gave up, and stays so; gdn_kv_attention_status() reads it.
+ *          gave up, and stays so; gdn_kv_attention_status() reads it.  (Only that
+ *          word needs the zeroes, and only for that: the kernels write the rest first.)
  * Products are exact in the codes, sums are fp32.  q, times a power of two for
  * each row, is exact while within 2^-10 of the row's largest.  A softmax weight,
  * times its block's value scale, is held
@@ -764,6 +765,13 @@ int gdn_kv_attention(const gdn_kv_shape* shape, int32_t T, const gdn_bf16* q, in
  * GDN_ERR_TIMEOUT when a bounded device wait gave up and the results of that call are
  * not valid (zero the workspace before its next use). */
 int gdn_kv_attention_status(const void* workspace, void* stream, int32_t* status);
+
+/* gdn_kv_attention_device_status -- the same of every gdn_kv_attention call on
+ * the current device since the word was last read, whichever workspace they
+ * used (one that the caller does not keep, say): waits for `stream`, reads the
+ * library's word for the device and, if it was set, clears it.  Call it with the
+ * calls in question ordered before `stream`'s end. */
+int gdn_kv_attention_device_status(void* stream, int32_t* status);
 
 #ifdef __cplusplus
 }
