@@ -492,8 +492,11 @@ int gdn_kv_plan(const gdn_kv_shape* shape, const int32_t* lens, const int32_t* a
     if ((rc = check_kv_shape(shape)) != GDN_OK) return rc;
     if (shape->B > kPlanMaxB)
         return report_error(GDN_ERR_UNSUPPORTED_SHAPE, "B=%d requests, one plan takes at most %d", shape->B, kPlanMaxB);
-    if ((int64_t)shape->width * shape->page > 0x7fffffffLL)
-        return report_error(GDN_ERR_UNSUPPORTED_SHAPE, "width=%d pages of %d tokens exceed 2^31 - 1 tokens", shape->width, shape->page);
+    if ((int64_t)shape->width * shape->page > kKvMaxCount)
+        return report_error(GDN_ERR_UNSUPPORTED_SHAPE, "width=%d pages of %d tokens exceed %lld tokens", shape->width, shape->page,
+                            (long long)kKvMaxCount);
+    if (rows > kKvMaxCount || free_cap > kKvMaxCount)
+        return report_error(GDN_ERR_UNSUPPORTED_SHAPE, "rows=%d or free_cap=%d above %lld", rows, free_cap, (long long)kKvMaxCount);
     if (rows < 0 || free_cap < 0) return report_error(GDN_ERR_INVALID_ARG, "negative size rows=%d free_cap=%d", rows, free_cap);
     const bool some = shape->B > 0;
     if ((some && ((rc = check_pointer(lens, "lens")) || (rc = check_pointer(add, "add")) || (rc = check_pointer(held, "held")) ||
@@ -537,6 +540,7 @@ int gdn_kv_append(const gdn_kv_shape* shape, int32_t T, const gdn_bf16* k, int64
     int rc;
     if ((rc = check_kv_shape(shape)) != GDN_OK) return rc;
     if (T < 0 || n_src < 0) return report_error(GDN_ERR_INVALID_ARG, "negative size T=%d n_src=%d", T, n_src);
+    if (T > kKvMaxCount) return report_error(GDN_ERR_UNSUPPORTED_SHAPE, "T=%d above %lld", T, (long long)kKvMaxCount);
     if (shape->Hkv > 65535) return report_error(GDN_ERR_UNSUPPORTED_SHAPE, "Hkv=%d exceeds the grid limit 65535", shape->Hkv);
     const int64_t row = (int64_t)shape->Hkv * shape->d;
     if ((rc = check_row_stride(ldk, row, "ldk")) || (rc = check_row_stride(ldv, row, "ldv"))) return rc;
@@ -582,8 +586,9 @@ int gdn_kv_attention(const gdn_kv_shape* shape, int32_t T, const gdn_bf16* q, in
     int rc;
     if ((rc = check_kv_shape(shape)) != GDN_OK) return rc;
     if (T < 0) return report_error(GDN_ERR_INVALID_ARG, "T=%d < 0", T);
-    if ((int64_t)T * (shape->Hq / shape->Hkv) > 0x7fffffffLL || (int64_t)shape->width * shape->page > 0x7fffffffLL)
-        return report_error(GDN_ERR_UNSUPPORTED_SHAPE, "T=%d rows or width=%d pages exceed 2^31 - 1 rows or tokens", T, shape->width);
+    if ((int64_t)T * (shape->Hq / shape->Hkv) > kKvMaxCount || (int64_t)shape->width * shape->page > kKvMaxCount)
+        return report_error(GDN_ERR_UNSUPPORTED_SHAPE, "T=%d rows or width=%d pages exceed %lld rows (of a group) or tokens", T, shape->width,
+                            (long long)kKvMaxCount);
     if ((rc = check_row_stride(ldq, (int64_t)shape->Hq * shape->d, "ldq")) != GDN_OK) return rc;
     if (!(scale > 0.0f) || scale > 1e6f) return report_error(GDN_ERR_INVALID_ARG, "scale=%g outside (0, 1e6]", (double)scale);
     if (T == 0 || shape->B == 0) return GDN_OK;  // nothing to do; pointers may be NULL

@@ -12,6 +12,11 @@
 
 namespace gdn {
 
+// The most rows, free pages and tokens of a table row that a call takes.  The
+// kernels count them in 32 bits and step past the last: by a grid's stride
+// (a thread to a row), by the tiles that they look ahead.
+constexpr int64_t kKvMaxCount = 0x7ff00000;
+
 // A block's scale is 2^e.  e4m3's largest number is 448 = 1.75 * 2^8.
 constexpr int kScaleMinExp = -100, kScaleMaxExp = 120;
 

@@ -647,7 +647,8 @@ int gdn_snapshot_restore(const gdn_shape* shape, int32_t layers, int32_t seq, co
  * table, table int32 [B, width].  A step is gdn_kv_plan (once), then
  * gdn_kv_append and gdn_kv_attention for each layer.
  * Shapes: d in {128, 256}; page in {32, 64, 128}; Hq a multiple of Hkv;
- * pages * Hkv * page < 2^31 - 256.  Query head h reads key/value head
+ * pages * Hkv * page < 2^31 - 256; a call's rows (in attention times Hq / Hkv),
+ * free_cap and width * page at most 2^31 - 2^20.  Query head h reads key/value head
  * h / (Hq / Hkv).  Slots: token position p of a request lies in slot
  * table[b][p / page] * page + p % page.
  */
