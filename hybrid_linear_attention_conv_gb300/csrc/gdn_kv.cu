@@ -196,6 +196,9 @@ __device__ __forceinline__ uint2 codes8(uint4 x, float f, bool finite) {
     return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
+// The largest magnitudes of two bf16 pairs among m and 8 bf16.
+__device__ __forceinline__ uint32_t max_abs8(uint32_t m, uint4 x) { return max_abs2(max_abs2(max_abs2(max_abs2(m, x.x), x.y), x.z), x.w); }
+
 // The largest finite |x| of 8 bf16, as bits, where some are not finite.
 __device__ __forceinline__ uint32_t max_finite8(uint32_t m, uint4 x) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -226,12 +229,13 @@ __device__ __forceinline__ void append_run(const KvAppendParams& p, int t, int n
     const int at = (int)(slot & ((1 << p.log2_page) - 1));
     float* scale = (is_v ? p.v_scale : p.k_scale) + page * p.Hkv + head;
     uint8_t* block = (is_v ? p.v_cache : p.k_cache) + ((page * p.Hkv + head) << p.log2_page) * p.d;
-    const float old = at > 0 ? *scale : 0.0f;  // read before the maximum's barrier, replaced after it
+    // read before the maximum's barrier, replaced after it
+    const float old = at > 0 ? __uint_as_float(scale_before(__float_as_uint(*scale), at)) : 0.0f;
     // chunk who + i * threads: row r0 + i * step of the run, always the same columns
     const int r0 = who >> shift, step = threads >> shift;
     const uint16_t* col = src + (who & (per_row - 1)) * 8;
     uint4 x[CH];
-    uint32_t m2 = 0, missing = 0;
+    uint32_t m2 = 0;
     if (p.rows == nullptr) {
         const uint16_t* from = col + (int64_t)(t + r0) * ld;
         const int64_t stride = (int64_t)step * ld;
@@ -243,14 +247,14 @@ __device__ __forceinline__ void append_run(const KvAppendParams& p, int t, int n
             x[i] = make_uint4(0, 0, 0, 0);
             if (r0 + i * step < n) {
                 const int row = p.rows[t + r0 + i * step];
-                if (row < 0 || row >= p.n_src) missing = 0x7f80u;  // a source row that is not there: the block's scale becomes NaN
+                if (row < 0 || row >= p.n_src) x[i] = make_uint4(~0u, ~0u, ~0u, ~0u);  // a source row that is not there is not finite
                 else x[i] = *reinterpret_cast<const uint4*>(col + (int64_t)row * ld);
             }
         }
     }
 #pragma unroll
-    for (int i = 0; i < CH; ++i) m2 = max_abs2(max_abs2(max_abs2(max_abs2(m2, x[i].x), x[i].y), x[i].z), x[i].w);
-    uint32_t top = reduce_max(max(max(m2 & 0xffffu, m2 >> 16), missing));
+    for (int i = 0; i < CH; ++i) m2 = max_abs8(m2, x[i]);
+    uint32_t top = reduce_max(max(m2 & 0xffffu, m2 >> 16));
     const bool finite = top < 0x7f80u;
     if (!finite) {
         uint32_t f = 0;
@@ -276,7 +280,18 @@ __device__ __forceinline__ void append_run(const KvAppendParams& p, int t, int n
 #pragma unroll
     for (int i = 0; i < CH; ++i)
         if (r0 + i * step < n) to[i * threads] = codes8(x[i], inv, finite);
-    if (who == 0) *scale = finite && !poisoned ? now : __int_as_float(0x7fffffff);
+    uint32_t bits = poisoned ? kLostScale : __float_as_uint(now);
+    if (!finite) {
+        uint32_t left = 0;  // rows from the first that is not finite on, for the maximum
+#pragma unroll 1
+        for (int r = r0; r < n && left == 0; r += step) {  // read again: rare, and the registers were full
+            const int row = p.rows == nullptr ? t + r : p.rows[t + r];
+            const uint32_t m = row < 0 || row >= p.n_src ? ~0u : max_abs8(0, *reinterpret_cast<const uint4*>(col + (int64_t)row * ld));
+            if (max(m & 0x7fffu, m >> 16 & 0x7fffu) >= 0x7f80u) left = n - r;
+        }
+        bits = marked_scale(bits, at + n - (int)reduce_max(left));
+    }
+    if (who == 0 && !(poisoned && old != old)) *scale = __uint_as_float(bits);  // (a NaN stays the one that it is)
 }
 
 template <int CH>

@@ -28,6 +28,23 @@ __host__ __device__ inline int scale_exp_of_bf16(uint32_t bits) {
     return e < kScaleMinExp ? kScaleMinExp : e > kScaleMaxExp ? kScaleMaxExp : e;
 }
 
+// A block with a row that is not finite has a NaN for its scale, whose payload
+// keeps what its other rows need should that row be taken back (a rejected draft):
+// the scale's biased exponent in bits 0 to 7 and the first such row in bits 8 to 14.
+// A scale that is no power of two (the caller's own) leaves a NaN without.
+constexpr uint32_t kLostScale = 0x7fffffffu, kMarkedScale = 0x7fc08000u;
+__host__ __device__ inline uint32_t marked_scale(uint32_t scale_bits, int row) {
+    const uint32_t e = scale_bits >> 23;
+    return (scale_bits & 0x807fffffu) != 0 || e == 0 || e == 255 ? kLostScale : kMarkedScale | (uint32_t)row << 8 | e;
+}
+// The scale of the rows before row `at`, as bits: a marked block's where its first row
+// that is not finite is none of them.
+__host__ __device__ inline uint32_t scale_before(uint32_t scale_bits, int at) {
+    const bool marked = (scale_bits & 0xffff8000u) == kMarkedScale;
+    const uint32_t e = scale_bits & 0xff;
+    return marked && e != 0 && e != 255 && (int)(scale_bits >> 8 & 0x7f) >= at ? e << 23 : scale_bits;
+}
+
 // Row coordinate of tokens [pos, pos + 32) of a sequence in the cache seen as
 // rows of d codes: rows of a page's head are adjacent.  A page that the table
 // does not have (outside the table's width or the cache) gives `rows`, one

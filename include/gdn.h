@@ -706,8 +706,12 @@ int gdn_kv_plan(const gdn_kv_shape* shape, const int32_t* lens, const int32_t* a
  * amax <= 448 * 2^e over the run's |k| (e in [-100, 120]); a block with earlier
  * tokens keeps its scale or grows to that, and its earlier codes are re-rounded
  * to the new scale.  Each code is the e4m3 number nearest to value / scale, to
- * even.  A run with a value that is not finite makes its block's scale NaN (the
- * block reads as NaN until it is begun again); codes are always finite.
+ * even.  A run with a value that is not finite makes its block's scale NaN: the
+ * block reads as NaN, all of it, until it is begun again or a run begins at or before the
+ * first such row, which takes that row back (the NaN's payload keeps the scale; one that
+ * is no power of two, the caller's own, is lost with it).  Codes are always finite.
+ * So draft rows that a round rejects leave one mark on the tokens before them in their
+ * page: a scale that has grown for them stays grown, and the codes rounded to it.
  * A page may take part in one run of a call only (as gdn_kv_plan's slots do).
  */
 int gdn_kv_append(const gdn_kv_shape* shape, int32_t T, const gdn_bf16* k, int64_t ldk, const gdn_bf16* v, int64_t ldv,
