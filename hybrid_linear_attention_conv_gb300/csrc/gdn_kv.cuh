@@ -1,6 +1,6 @@
 // gdn_kv.cuh -- what the paged 8-bit cache's kernels share: the launch
 // parameters that gdn_kv.cu fills after validation, the power-of-two scales,
-// and the split of a value into two e4m3 numbers.  Nothing here is part of
+// and the split of a value into two 8-bit numbers.  Nothing here is part of
 // the ABI.
 #pragma once
 
@@ -195,12 +195,12 @@ __device__ __forceinline__ float2 float2_of_e4m3x2(uint32_t w) {
     return r;
 }
 
-// Four values, |x| <= 448, as e4m3 hi + lo: hi = RNE(x), lo = RNE(x - hi), where
-// x - hi is exact.  hi + lo holds eight significant bits of |x| >= 2^-2 and is
-// within 2^-10 of smaller ones (lo's smallest step is 2^-9), so a bf16 value is
-// held exactly while it is within 2^-10 of its row's largest.  The values go by
-// way of f16 pairs, whose conversions are half the instructions: that rounds by
-// 2^-12 of x, and not at all where x has eleven significant bits or fewer.
+// Four bf16 values, |x| <= 448, as hi (e4m3) + lo (e5m2): hi = RNE(x), and
+// x - hi is at most eight steps of x, which e5m2's three significant bits hold
+// exactly while x is above 2^-6; below, hi + lo is within 2^-14 of x (half a step of lo
+// next to half a step of hi, 2^-10).  So a bf16 value is held exactly while it is
+// within 2^-14 of its row's largest.  The values go by way of f16 pairs, whose
+// conversions are half the instructions: exact, but for 2^-25 of what is that small.
 __device__ __forceinline__ uint32_t f16x2(float a, float b) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
@@ -216,11 +216,16 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ void split4_f16(float e0, float e1, float e2, float e3, uint32_t& hi, uint32_t& lo) {
+__device__ __forceinline__ uint32_t e5m2x2_of_f16x2(uint32_t w) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(w));
+    return r;
+}
+__device__ __forceinline__ void split4_queries(float e0, float e1, float e2, float e3, uint32_t& hi, uint32_t& lo) {
     const uint32_t a = f16x2(e0, e1), b = f16x2(e2, e3);
     const uint32_t ha = e4m3x2_of_f16x2(a), hb = e4m3x2_of_f16x2(b);
-    const uint32_t la = e4m3x2_of_f16x2(sub_f16x2(a, f16x2_of_e4m3x2(ha)));
-    const uint32_t lb = e4m3x2_of_f16x2(sub_f16x2(b, f16x2_of_e4m3x2(hb)));
+    const uint32_t la = e5m2x2_of_f16x2(sub_f16x2(a, f16x2_of_e4m3x2(ha)));
+    const uint32_t lb = e5m2x2_of_f16x2(sub_f16x2(b, f16x2_of_e4m3x2(hb)));
     hi = ha | (hb << 16);
     lo = la | (lb << 16);
 }

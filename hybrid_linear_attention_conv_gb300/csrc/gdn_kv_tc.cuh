@@ -7,9 +7,9 @@
 namespace gdn {
 namespace tc {
 
-// Instruction descriptor, kind::f8f6f4: e4m3 A and B (K-major), fp32 D.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
-    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// Instruction descriptor, kind::f8f6f4: e4m3 or (a_e5m2) e5m2 A, e4m3 B, both K-major, fp32 D.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, bool a_e5m2) {
+    return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 // Shared-memory matrix descriptor of an MN-major operand of 8-bit elements with
@@ -26,8 +26,8 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t 
     return d;
 }
 
-// D (+)= A B for one K = 32 step of e4m3 operands.
-__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+// D (+)= A B for one K = 32 step of 8-bit operands.
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                          uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"

@@ -5,9 +5,9 @@
 //   t_j = scale log2(e) a_j (q . c_j) + log2 b_j,   o = sum 2^(t_j - m) w_j / sum 2^(t_j - m) / b_j.
 //
 // Both products take the cache's codes as they are: q and the weights are split
-// into two e4m3 numbers, hi + lo, and every contraction runs over both, twice
-// the products at twice bf16's rate, with half its bytes of operands and no
-// conversion of a tile.
+// into two 8-bit numbers, hi + lo (e4m3; q's lo is e5m2, which makes the pair exact), and
+// every contraction runs over both, twice the products at twice bf16's rate,
+// with half its bytes of operands and no conversion of a tile.
 //
 // The weights' product is the block-scaled kind (mxf8f6f4).  A row's weights of 32
 // tokens, which share a value scale b, are a block with a power of two of its own, 2^e with the
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t a = finite ? word[2 * k] : 0u, b = finite ? word[2 * k + 1] : 0u;
-                    split4_f16(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xffff0000u) * inv, __uint_as_float(b << 16) * inv,
+                    split4_queries(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xffff0000u) * inv, __uint_as_float(b << 16) * inv,
                                __uint_as_float(b & 0xffff0000u) * inv, hi[k], lo[k]);
                 }
                 const uint32_t at = (c >> 3) * (kM * 128) + local * 128 + (((c & 7) ^ (local & 7)) << 4);
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
         // d = 256, where the products take 1,024 each, one warp issues both, and the
         // tensor pipe's order keeps a tile's weights until their product has read
         // them; for d = 128 (512 each) a warp for each, the logits' one waiting for that product.
-        constexpr uint32_t id_s = tc::idesc_e4m3(kM, kN);
+        constexpr uint32_t id_hi = tc::idesc_f8(kM, kN, false), id_lo = tc::idesc_f8(kM, kN, true);
         const uint32_t ring = tc::smem_u32(sm.ring[0]);
         auto logits = [&](int g, int qb, bool last) {
             const int u = 2 * g, slot = u % kSlots, buf = g % kBufs;
@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_kv_attn_tiles_kernel(const __
 #pragma unroll
                     for (int ks = 0; ks < D / 32; ++ks) {
                         const uint32_t at = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
-                        tc::mma_e4m3(d, (part ? q_lo : q_hi) + at, k + at, id_s, part + ks > 0);
+                        tc::mma_f8(d, (part ? q_lo : q_hi) + at, k + at, part ? id_lo : id_hi, part + ks > 0);
                     }
                 tc::mma_commit(empty + 8 * slot);
                 tc::mma_commit(s_full + 8 * buf);

@@ -745,7 +745,7 @@ size_t gdn_kv_attention_workspace_bytes(const gdn_kv_shape* shape);
  *          gave up, and stays so; gdn_kv_attention_status() reads it.  (Only that
  *          word needs the zeroes, and only for that: the kernels write the rest first.)
  * Products are exact in the codes, sums are fp32.  q, times a power of two for
- * each row, is exact while within 2^-10 of the row's largest.  A softmax weight,
+ * each row, is exact while within 2^-14 of the row's largest.  A softmax weight,
  * times its block's value scale, is held
  *   by the kernel of 128 rows as two e4m3 numbers with a power of two for every row and 32
  *   tokens (position / 32): within 2^-8 of itself, or 2^-22 of the largest of those 32;

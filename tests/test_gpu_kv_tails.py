@@ -91,8 +91,8 @@ class Tail:
         last = slice((copies - 1) * self.n, copies * self.n)
         return out[last].double(), lse[last].double()
 
-    def check(self, tiles, f16=False, copies=1):
-        """f16: the bound of the kernel of eight rows at a time."""
+    def check(self, tiles, f16=False, copies=1, exact_q=False):
+        """f16: the bound of the kernel of eight rows at a time; exact_q: no element of q is rounded."""
         out, lse = self.run(tiles, copies)
         L, d = self.L, self.d
         a, b = (s.double().repeat_interleave(PAGE)[:L] for s in (self.ks, self.vs))
@@ -108,7 +108,7 @@ class Tail:
         blocks = torch.nn.functional.pad(w, (0, -L % 32)).unflatten(-1, (-1, 32))
         top = blocks.amax(-1, keepdim=True).expand_as(blocks).flatten(-2)[..., :L] * seen[:, None]
         q = self.q.double()
-        ds = d_scale(d) * a * (q.abs().amax(-1, keepdim=True) * 2.0 ** (-32 if f16 else -17) * k.abs().sum(-1) + d * 2.0 ** -23 * (q.abs() @ k.abs().T))
+        ds = d_scale(d) * a * (q.abs().amax(-1, keepdim=True) * (0.0 if exact_q else 2.0 ** (-32 if f16 else -17)) * k.abs().sum(-1) + d * 2.0 ** -23 * (q.abs() @ k.abs().T))
         ds = (ds + 2.0 ** -21 + (s + b.log2()).abs() * 2.0 ** -22).masked_fill(~seen[:, None], 0)
         moved = 2 * math.log(2) * ds.amax(-1, keepdim=True)
         sums = L / 16 * 2.0 ** -22
@@ -181,3 +181,18 @@ def test_eight_rows_keep_a_tail_far_below(bits, G, d):
     t.v[0] = 0
     t.lift(0, bits)
     t.check(False, f16=True, copies=1000)
+
+
+@pytest.mark.parametrize("tiles", [False, True])
+@pytest.mark.parametrize("new,G,d", FORMS)
+@pytest.mark.parametrize("large", [2.0 ** 8, 2.0 ** 12])
+def test_a_query_with_one_large_channel(large, new, G, d, tiles):
+    """Every other element of q is within 2^-14 of the large one, where q is exact: a channel
+    whose keys are zero changes nothing, however large."""
+    t = Tail(300, new, G, d, seed=int(large))
+    g = torch.Generator(device=DEV).manual_seed(3)
+    size = 0.5 + 1.5 * torch.rand((new, G, d), generator=g, device=DEV)
+    t.q = (size * torch.sign(t.q.float())).to(torch.bfloat16)
+    t.q[..., 0] = large
+    t.ks.fill_(2.0 ** -5)  # peaked: logits of some units
+    t.check(tiles, exact_q=True)
