@@ -163,11 +163,11 @@ __global__ void __launch_bounds__(kPlanThreads) gdn_kv_plan_kernel(KvPlanParams 
 // warp take each short run, and takes the long ones as a whole, a thread
 // holding its part of the run in registers between the maximum and the
 // conversion.
-// Measured in a graph, 4 heads of 256: 64 single tokens 4.1 us; 8,192 rows
-// 10.2 us = 4.9 TB/s (a CTA's life is load, maximum, barrier, conversion, store, and
+// Measured in a graph, 4 heads of 256: 64 single tokens 4.5 us; 8,192 rows
+// 10.0 us = 4.9 TB/s (a CTA's life is load, maximum, barrier, conversion, store, and
 // there are 1.7 CTAs for each that is resident: two waves, the second not full; the
 // conversion keeps the integer pipe 55 % busy).  37 chunks of up to 2,000 rows, 8 heads
-// of 128: 23.0 us = 3.5 TB/s, with pages begun and ended inside the chunks.
+// of 128: 23.5 us = 3.4 TB/s, with pages begun and ended inside the chunks.
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 256;
 constexpr int kAppendWarps = kAppendThreads / 32;
@@ -393,8 +393,12 @@ int check_row_stride(int64_t ld, int64_t row, const char* name) {
     return GDN_OK;
 }
 
-// Rows a CTA looks at.  Few rows are mostly single tokens, a warp each; of many
-// rows most belong to long runs, of which about one begins in every P rows.
+// Rows a CTA looks at.  Few rows are mostly single tokens, a warp each; the CTA
+// of a long run takes it as a whole, and one begins in about every P rows.  Which of
+// the two many rows are the host does not know.  Measured (us, eight rows a CTA and P), 4
+// heads of 256, pages of 128: 4,000 rows of long runs 17.9, 6.5, of single tokens 53.2,
+// 50.3; 1,025 rows 7.9, 4.9 and 16.5, 45.2: a decode batch just above 1,024 pays for
+// the prompts of its size.  Pages of 32: 1,025 rows 5.1, 3.4 and 11.4, 14.1.
 int append_tile_rows(int T, int P) { return T <= 1024 ? kAppendWarps : P; }
 
 // cuTensorMapEncodeTiled from the driver, looked up once.
@@ -450,10 +454,14 @@ bool encode_cache_map(CUtensorMap* map, const uint8_t* cache, const gdn_kv_shape
 // 1 << 20 / d where they are not.  All that the host knows of the lengths is the
 // table's width: where that bound is loose, both sides grow, and more than
 // eight rows a request go to the second.  Measured (rows, tiles, us): 64 requests of
-// 8,000 tokens, 24/4 heads of 256, 6 rows 165, 218; 12 rows 316, 220; one of
-// 8,000 tokens, 60 rows 25, 32; 252 rows 57, 34; a first prompt of 85 tokens 16, 27;
-// 64/4 heads of 128, 64 requests of 8,000, 16 rows 169, 150; over 199 such pairs
-// the rule loses 1.11x at most; eight rows a request as the border loses up to 2.7x.
+// 8,000 tokens, 24/4 heads of 256, 6 rows 169, 217; 12 rows 321, 218; one of
+// 8,000 tokens, 60 rows 25, 31; 252 rows 59, 33; a first prompt of 85 tokens 17, 27;
+// 64/4 heads of 128, 64 requests of 8,000, 16 rows 173, 146; over 199 such pairs
+// the rule loses 1.18x at most; eight rows a request as the border loses up to 2.7x.
+// Those are steps of requests alike: the rule goes by their mean, and one kernel takes all.  63
+// single tokens at 4,000 to 12,000 and 512 queries after 8,000, 24/4 heads of 256: 698, 287
+// (each in its own 180 + 89); 250 single tokens at 16,000 and 250 queries after as many, 32/8
+// heads of 128, which the mean leaves with the first: 1,497, 1,901 (1,254 + 79).
 bool use_tiles(const gdn_kv_shape* s, int T) {
     const double L = (double)s->width * s->page, heads = (double)s->B * s->Hkv;
     const double rows = std::ceil((double)T * (s->Hq / s->Hkv) / s->B);

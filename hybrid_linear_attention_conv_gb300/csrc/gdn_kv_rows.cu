@@ -43,10 +43,10 @@
 // stream of the cache had driven out of the L2.)
 //
 // Measured, 24/4 heads of 256, one token a request: 64 requests of 4,096 to 12,288
-// tokens 167 us = 6.3 TB/s of cache, 95 % of a plain copy's rate; one of 131,072 in
+// tokens 167 to 171 us (by box) = 6.3 to 6.2 TB/s of cache, 95 to 92 % of a plain copy's rate; one of 131,072 in
 // 55 us = 4.9 TB/s and of 4,097 in 11.4 us, where the chain of a launch (scan of
 // the requests, table entry, scales, first tile, join) shows.  32/8 heads of 128, 251
-// requests of up to 3,000: 133 us = 5.7 TB/s, with an item's ends once in 47 tiles.
+// requests of up to 3,000: 131 to 135 us = 5.8 to 5.6 TB/s, with an item's ends once in 47 tiles.
 #include <algorithm>
 #include <mutex>
 

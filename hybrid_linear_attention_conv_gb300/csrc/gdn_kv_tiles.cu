@@ -43,10 +43,12 @@
 // Bound by the tensor cores, 8 d flops a row and token (both products, hi and
 // lo) at twice bf16's rate, so 4 d at bf16's; for d = 128 by the softmax, whose
 // exponentials and moves are the same for half the products.  Measured: a
-// prompt of 8,192, 24/4 heads of 256, causal, 606 to 642 us (by box) = 1.36 to 1.28
+// prompt of 8,192, 24/4 heads of 256, causal, 578 to 637 us (by box) = 1.43 to 1.29
 // PFLOP/s of visible pairs, about 3,000 cycles a tile of 128 x 128 against
-// 2,048 of products; 1,024 queries after 30,000 tokens 511 us = 1.53 PFLOP/s.
-// d = 128: 2,200 cycles a tile against 1,024.  Small steps pay 20 to 25 us beside
+// 2,048 of products; 1,024 queries after 30,000 tokens 475 us = 1.62 PFLOP/s.
+// d = 128: 2,300 cycles a tile against 1,024 (1,024 queries of 32/8 heads after 30,000
+// tokens 458 us).  ptxas spills 100 B of stores a thread for d = 128 and 40 for 256
+// around the tile loop's 88 registers.  Small steps pay 20 to 25 us beside
 // their tiles: the list and the first q 7 to 10, an item's beginning and end, the
 // join's launch and reads.
 #include <algorithm>

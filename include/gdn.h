@@ -753,11 +753,13 @@ size_t gdn_kv_attention_workspace_bytes(const gdn_kv_shape* shape);
  * So a long flat tail is kept however much of the softmax another token has.
  * What lies in the cache past a request's length is never used, whatever its bits.
  * The sizes (T, the shape, and its width as the bound of the lengths) pick the
- * kernel, eight rows (queries x heads of a group) at a time or 128; the two
- * differ in last bits.  Up to eight rows a request, T * Hq / Hkv <= 8 * B, it is the
- * first; above, a table no wider than the lengths need lets small steps stay
- * with it where it is the faster.  Results do not depend on timing: the same
- * call gives the same bits.
+ * kernel, eight rows (queries x heads of a group) at a time or 128, for all of
+ * the step's requests; the two differ by the roundings above.  Up to eight rows a request on
+ * average, T * Hq / Hkv <= 8 * B, it is the first; above, a table no wider than the
+ * lengths need lets small steps stay with it where it is the faster.  (Where a
+ * step's requests have very different numbers of queries, a call for the ones of few and a
+ * call for the ones of many can be faster than one for all.)  Results do not depend on
+ * timing: the same call gives the same bits.
  * The kernels are programmatic dependent launches, as gdn_conv_decode_step's.
  */
 int gdn_kv_attention(const gdn_kv_shape* shape, int32_t T, const gdn_bf16* q, int64_t ldq, const uint8_t* k_cache,
