@@ -734,7 +734,8 @@ size_t gdn_kv_attention_workspace_bytes(const gdn_kv_shape* shape);
  *   q      bf16 [T, Hq, d], ldq elements between rows (a multiple of 8).
  *   table, start, lens  as gdn_kv_plan leaves them (lens after the step).
  *   tree   int64 [T], or NULL (causal).
- *   scale  in (0, 1e6].   k_scale, v_scale positive and finite, 2^-100 .. 2^120
+ *   scale  in (0, 1e6].   k_scale, v_scale positive and finite, 2^-100 .. 2^120,
+ *          the value scales that a row sees within 2^110 of one another
  *          (a NaN scale makes the rows that see its block NaN, and so does a
  *          table entry outside the cache).
  *   out    bf16 [T, Hq, d], rounded once.   lse fp32 [T, Hq], or NULL.

@@ -196,3 +196,43 @@ def test_a_query_with_one_large_channel(large, new, G, d, tiles):
     t.q[..., 0] = large
     t.ks.fill_(2.0 ** -5)  # peaked: logits of some units
     t.check(tiles, exact_q=True)
+
+
+@pytest.mark.parametrize("tiles", [False, True])
+@pytest.mark.parametrize("new,G,d", FORMS)
+@pytest.mark.parametrize("lo,hi", [(-40, 40), (-100, 10), (0, 110)])
+def test_value_scales_far_apart(lo, hi, new, G, d, tiles):
+    """Every page with a value scale of its own: the pages of the largest make the output, all
+    of them the sum."""
+    L = 3000
+    t = Tail(L, new, G, d, seed=hi)
+    g = torch.Generator(device=DEV).manual_seed(hi)
+    t.vs = torch.exp2(torch.randint(lo, hi + 1, t.vs.shape, generator=g, device=DEV).float())
+    t.vs[0], t.vs[1], t.vs[-1] = 2.0 ** lo, 2.0 ** hi, 2.0 ** lo
+    t.check(tiles)
+
+
+@pytest.mark.parametrize("tiles", [False, True])
+@pytest.mark.parametrize("new,G,d", FORMS)
+@pytest.mark.parametrize("bits,seed", [(12, 0), (60, 1), (300, 2), (300, 3)])
+def test_logits_that_jump_from_tile_to_tile(bits, seed, new, G, d, tiles):
+    """Stretches of 32 to 256 tokens whose logits lie up to `bits` powers of two apart, up and down."""
+    L = 5000
+    t = Tail(L, new, G, d, seed=seed)
+    g = torch.Generator().manual_seed(seed)
+    level, i = torch.zeros(t.k.shape[0]), 0
+    while i < L:
+        n = 32 * int(torch.randint(1, 9, (), generator=g))
+        level[i:i + n] = float(torch.randint(-448, 449, (), generator=g))
+        i += n
+    t.k[:, 0] = nearest(level).to(DEV)
+    t.q[..., 0] = bits / 2 / (d_scale(d) * 2.0 ** -7 * 448.0)
+    t.check(tiles)
+
+
+@pytest.mark.parametrize("tiles", [False, True])
+@pytest.mark.parametrize("L,new", [(1, 1), (2, 2), (33, 33), (127, 3), (129, 129), (200, 1)])
+@pytest.mark.parametrize("G,d", [(6, 256), (5, 128)])
+def test_short_requests(L, new, G, d, tiles):
+    t = Tail(L, new, G, d, seed=L)
+    t.check(tiles)
