@@ -632,8 +632,8 @@ def prefill_status(workspace: torch.Tensor) -> int:
 
 
 def set_wait_limit_ns(ns: int) -> int:
-    """Limit of every bounded device wait of the prefill kernels (process-wide,
-    read at each later launch); returns the previous limit."""
+    """Limit of every bounded device wait of the prefill's and the cache attention's kernels
+    (process-wide, read at each later launch); returns the previous limit."""
     return int(load().gdn_set_wait_limit_ns(int(ns)))
 
 

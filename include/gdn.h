@@ -535,8 +535,8 @@ int gdn_prefill_status(const void* workspace, void* stream, int32_t* status);
 
 /*
  * gdn_set_wait_limit_ns -- the limit, in nanoseconds, of every bounded device
- * wait of the prefill kernels (for the tensor cores, a copy, or another CTA's
- * pre-pass record), read at each later launch; returns the previous limit.
+ * wait of the prefill's and the cache attention's kernels (for the tensor cores, a
+ * copy, or another CTA's pre-pass record), read at each later launch; returns the previous limit.
  * Default 200,000,000 (0.2 s); values above 10 s are clamped to 10 s; 0 makes
  * a wait give up at once unless what it waits for has already happened (for
  * tests of the timeout path).  A wait that gives up sets the call's status
