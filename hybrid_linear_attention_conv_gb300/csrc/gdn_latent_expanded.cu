@@ -432,14 +432,16 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_latent_expanded_kernel(const 
             if (!more) break;
             it = it_next;
         }
-        // the end, and, after a wait that gave up, everything on its way
+        // The end, in a place that is free.  After a wait that gave up it may still be the place of a block whose output
+        // goes by it: it stays as it is, and the other warps, which look at `dead` behind every block, leave by that.
         const int slot = count & 1;
         if (count >= 2) wait(item_empty + 8 * slot, count / 2 - 1);
         if (lane == 0) {
-            sm.item[slot].h = -1;
+            if (!*dead) sm.item[slot].h = -1;
             tc::mbar_arrive(item_full + 8 * slot);
         }
         __syncwarp();
+        // and, after a wait that gave up, everything on its way
         if (*dead) {
             tc::mbar_wait(next_full, asked & 1, kDrainNs);  // (done, if its answer has been read)
             if (sent_q > 0) tc::mbar_wait(q_full, (sent_q - 1) & 1, kDrainNs);
