@@ -441,12 +441,10 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_latent_expanded_kernel(const 
             tc::mbar_arrive(item_full + 8 * slot);
         }
         __syncwarp();
-        // and, after a wait that gave up, everything on its way
-        if (*dead) {
-            tc::mbar_wait(next_full, asked & 1, kDrainNs);  // (done, if its answer has been read)
-            if (sent_q > 0) tc::mbar_wait(q_full, (sent_q - 1) & 1, kDrainNs);
-            for (int i = max(0, sent - kRing); i < sent; ++i) tc::mbar_wait(full + 8 * (i % kRing), (i / kRing) & 1, kDrainNs);
-        }
+        // Everything on its way lands before the CTA ends, also that of a block whose other warps' waits give up after this.
+        tc::mbar_wait(next_full, asked & 1, kDrainNs);  // (done, if its answer has been read)
+        if (sent_q > 0) tc::mbar_wait(q_full, (sent_q - 1) & 1, kDrainNs);
+        for (int i = max(0, sent - kRing); i < sent; ++i) tc::mbar_wait(full + 8 * (i % kRing), (i / kRing) & 1, kDrainNs);
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
         // ------------------------------------------------------------ MMAs of one tile of queries
         constexpr uint32_t id_s = tc::idesc_bf16(kM, kN), id_o = tc::idesc_bf16(kM, 64) | 1u << 16;  // values MN-major

@@ -96,3 +96,19 @@ def test_expanded_writes_nothing_outside(H, lens, new):
     call(*inside.views)
     want = [v[first:first + T].clone() for v in inside.views]
     under_limits(call, inside, want, sentinel())
+
+
+@pytest.mark.parametrize("H,lens,new", [(160, [3000], [100]), (152, [128 * 5], [128]), (32, [2000] * 5, [3] * 5)], ids=str)
+def test_expanded_last_blocks_copies_land(H, lens, new):
+    """A block or two to a CTA, whose loader is through with its copies long before they are used: a wait that gives up then
+    must not end the CTA before they have landed (in what may be another's shared memory by then)."""
+    c = expanded_case(23, H, lens, new)
+    T = sum(new)
+
+    def call(out, lse):
+        gdn.latent_attention_expanded(c["q"], c["k"], c["k_rope"], c["v"], c["start"], c["key_start"], SCALE, out=out, lse=lse)
+
+    inside = Inside(T, H, 128, 0, T)
+    call(*inside.views)
+    want = [v.clone() for v in inside.views]
+    under_limits(call, inside, want, sentinel())
