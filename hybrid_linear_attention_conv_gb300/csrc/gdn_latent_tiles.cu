@@ -71,7 +71,7 @@ struct LatentSmem {
     short query[N];                      // the rows' queries, from the first one's on, -1 where there is none
     alignas(8) int limit[N];             // without a tree: a row sees the tokens before this
     alignas(8) uint64_t full[kRing], empty[kRing], info_full[kInfo], s_full[2], p_ready[2], o_done[2];
-    uint64_t key_full, key_empty, q_full, q_empty, item_done, o_free, drained[2];
+    uint64_t key_full, key_empty, q_full, q_empty, item_done, sums_there, o_free, drained[2];
     int bad[kInfo];                      // a tile's pages that are not in the cache, by 32 tokens
     int at_b, at_t, at_v;
     uint32_t tmem;
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_latent_tiles_kernel(const __g
     const uint32_t full = tc::smem_u32(sm.full), empty = tc::smem_u32(sm.empty), key_full = tc::smem_u32(&sm.key_full),
                    key_empty = tc::smem_u32(&sm.key_empty), info_full = tc::smem_u32(sm.info_full), s_full = tc::smem_u32(sm.s_full),
                    p_ready = tc::smem_u32(sm.p_ready), o_done = tc::smem_u32(sm.o_done), q_full = tc::smem_u32(&sm.q_full),
-                   q_empty = tc::smem_u32(&sm.q_empty), item_done = tc::smem_u32(&sm.item_done), o_free = tc::smem_u32(&sm.o_free),
+                   q_empty = tc::smem_u32(&sm.q_empty), item_done = tc::smem_u32(&sm.item_done), sums_there = tc::smem_u32(&sm.sums_there), o_free = tc::smem_u32(&sm.o_free),
                    drained = tc::smem_u32(sm.drained);
     if (tid == 0) {
         tc::prefetch_map(&p.tm);
@@ -272,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_latent_tiles_kernel(const __g
         tc::mbar_init(q_full, kQWarps);
         tc::mbar_init(q_empty, 1);
         tc::mbar_init(item_done, 1);
+        tc::mbar_init(sums_there, kSoftWarps);
         tc::mbar_init(o_free, kQWarps);
     }
     if (warp == kKeyWarp) tc::tmem_alloc(tc::smem_u32(&sm.tmem), 512);
@@ -558,7 +559,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_latent_tiles_kernel(const __g
                 const bool whole = tile0 / W == (tile0 + w.kt - 1) / W;
                 uint16_t* out = p.out + ((int64_t)w.r.row0 * p.H + first) * kLatent + quad * 32;
                 float* part = p.partials + ((size_t)blockIdx.x * 2 + (w.j0 == 0 ? 1 : 0)) * kPart + quad * 32 + lane;
-                tc::named_sync(2, (kSoftWarps + kQWarps) * 32);  // the sums are there
+                // (A barrier in shared memory, bounded as every wait between roles: at a hardware barrier the softmax's warps, which
+                // do not wait there, would meet themselves once a wait that gave up has let them come twice, and these for ever.)
+                wait(sums_there, item);
                 wait(item_done, item);
                 tc::fence_after_sync();
                 float o[2][16];
@@ -783,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_latent_tiles_kernel(const __g
                 }
             }
             __syncwarp();
-            tc::named_arrive(2, (kSoftWarps + kQWarps) * 32);
+            if (lane == 0) tc::mbar_arrive(sums_there);
             if (c0 != c1 && w.j0 == 0 && tid == 0) {  // the item begins here: what the join needs
                 p.spans[blockIdx.x] = c1 - c0;
                 p.span_rows[blockIdx.x * 2] = at;

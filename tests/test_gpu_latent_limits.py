@@ -112,3 +112,22 @@ def test_expanded_last_blocks_copies_land(H, lens, new):
     call(*inside.views)
     want = [v.clone() for v in inside.views]
     under_limits(call, inside, want, sentinel())
+
+
+# items of 16, 32 and 64 rows, several to a CTA, of one tile and of many, whole and in parts; causal and by tree
+@pytest.mark.parametrize("H,lens,new", [(8, [100] * 700, [1] * 700), (64, [200, 30] * 60, [1, 2] * 60), (128, [700] * 30, [1] * 30),
+                                        (20, [3000, 64, 500] * 20, [1, 1, 3] * 20), (64, [300] * 8, [40] * 8)], ids=str)
+def test_absorbed_ends_and_writes_nothing_outside(H, lens, new):
+    c = latent_case(24, H, 64, lens, new)
+    T, first = sum(new), 3
+    q, r = (torch.cat([x[:first], x, x[:2]]) for x in (c["q"], c["q_rope"]))
+    start = i32([first + x for x in starts(new)])
+    ws = torch.zeros(gdn.latent_attention_workspace_bytes(), dtype=torch.uint8, device=DEV)
+
+    def call(out, lse):
+        gdn.latent_attention(q, r, c["cache"], c["table"], start, c["lens"], SCALE, out=out, lse=lse, workspace=ws)
+
+    inside = Inside(T + first + 2, H, 512, first, first + T)
+    call(*inside.views)
+    want = [v[first:first + T].clone() for v in inside.views]
+    under_limits(call, inside, want, sentinel())
