@@ -226,6 +226,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_latent_expanded_kernel(const 
         }
     };
 
+    // Whether the CTA's copies have ended, the same answer for a warp's lanes: what they then do or leave out has votes in it.
+    auto over = [&]() { return __any_sync(~0u, *dead != 0) != 0; };
+
     // A wait for a barrier in each lane at once (each that has one to wait for).
     auto wait_lanes = [&](bool mine, uint32_t bar, uint32_t parity) {
         const bool there = !mine || tc::mbar_test(bar, parity & 1);
@@ -351,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_latent_expanded_kernel(const 
         // the block after this one, and the question for the one after that
         auto look_ahead = [&]() {
             wait(next_full, asked);
-            if (*dead) {  // (the answer may be on its way: waited for below)
+            if (over()) {  // (the answer may be on its way: waited for below)
                 more = false;
                 return;
             }
@@ -379,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_latent_expanded_kernel(const 
             } else {
                 const int slot = count & 1;
                 if (count >= 2) wait(item_empty + 8 * slot, count / 2 - 1);
-                if (*dead) break;  // (its place may still be read)
+                if (over()) break;  // (its place may still be read)
                 if (lane == 0) {
                     sm.item[slot] = it;
                     tc::mbar_arrive(item_full + 8 * slot);
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_latent_expanded_kernel(const 
                 auto unit = [&](const CUtensorMap* map, int x, int h, int y) {
                     const int s = u % kRing;
                     if (u >= kRing) wait(empty + 8 * s, u / kRing - 1);
-                    if (!*dead) {
+                    if (!over()) {
                         sent = u + 1;
                         if (tc::elect_one()) {
                             tc::mbar_arrive_expect_tx(full + 8 * s, kGroup);
@@ -401,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_latent_expanded_kernel(const 
                     ++u;
                 };
                 if (count > 0) wait(q_empty, count - 1);
-                if (!*dead) {
+                if (!over()) {
                     sent_q = count + 1;
                     if (tc::elect_one()) {
                         tc::mbar_arrive_expect_tx(q_full, 2 * kKeyUnits * kGroup);
@@ -460,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_latent_expanded_kernel(const 
             const Item it = sm.item[count & 1];
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(item_empty + 8 * (count & 1));
-            if (it.h < 0 || *dead) break;
+            if (over() || it.h < 0) break;
             const Part part = part_of(it, side);
             const int tiles = part.tiles, from_guard = first_guarded(it, tiles);
             const int all_see = max(0, min(it.L, it.L - it.n + part.first + 1));
@@ -534,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_latent_expanded_kernel(const 
             const Item it = sm.item[count & 1];
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(item_empty + 8 * (count & 1));
-            if (it.h < 0 || *dead) break;
+            if (over() || it.h < 0) break;
             const int tiles = part_of(it, 0).tiles;
             const int from_guard = first_guarded(it, tiles);
             for (int j = 0; j < tiles; ++j) {

@@ -348,6 +348,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_latent_tiles_kernel(const __g
         }
     };
 
+    // Whether the CTA's copies have ended, the same answer for a warp's lanes: what they then do or leave out has votes in it.
+    auto over = [&]() { return __any_sync(~0u, *dead != 0) != 0; };
+
     // The same for a barrier in each lane at once (each that has one to wait for).
     auto wait_lanes = [&](bool mine, uint32_t bar, uint32_t parity) {
         const bool there = !mine || tc::mbar_test(bar, parity & 1);
@@ -405,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_latent_tiles_kernel(const __g
                 };
                 if (g > 0) wait(key_empty, g - 1);
                 // Never into a slot whose wait gave up: a second arrival in a phase that still awaits its bytes is a fault.
-                if (!*dead) {
+                if (!over()) {
                     sent_keys = g + 1;
                     if (tc::elect_one()) {
                         tc::mbar_arrive_expect_tx(key_full, kBox);
@@ -430,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_latent_tiles_kernel(const __g
                 for (int i = 0; i < kUnits; ++i) {
                     const int u = g * kUnits + i, slot = u % kRing;
                     if (u >= kRing) wait(empty + 8 * slot, u / kRing - 1);
-                    if (*dead) continue;
+                    if (over()) continue;
                     sent_units = u + 1;
                     if (tc::elect_one()) {
                         tc::mbar_arrive_expect_tx(full + 8 * slot, kUnit);
