@@ -645,9 +645,11 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_latent_tiles_kernel(const __g
                     tmem_ld_fragments(tmem + lanes + (g & 1) * N, s);
                     if (masked) {
                         if (pass == 0) {
-                            // A token whose row is not finite has no finite logit in any column (those without a row, of
+                            // A token whose values are not finite has no finite logit in any column (those without a row, of
                             // zeros, among them): zeros in its place for the second product, and NaN for the rows that see it.
                             // (So it goes for what lies past the request's end, too; finite values there meet weights of zero.)
+                            // Logits alone say it of a row whose key part is not finite, or whose sums leave fp32's range, too: its
+                            // values are looked at, below, and where they are finite its weights are what its logits make them.
                             bool gone[2] = {true, true};
 #pragma unroll
                             for (int i = 0; i < N / 2; ++i) gone[(i >> 1) & 1] = gone[(i >> 1) & 1] && !(fabsf(s[i]) < INFINITY);
@@ -687,10 +689,25 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_latent_tiles_kernel(const __g
                                 unsigned rows_gone = __ballot_sync(~0u, (lane & 3) == 0 && (lost >> 2 * k & 1));
 #pragma unroll 1
                                 while (rows_gone) {
-                                    const int t = warp * 16 + ((__ffs(rows_gone) - 1) >> 2) + 8 * k;
+                                    const int four = (__ffs(rows_gone) - 1) >> 2, t = warp * 16 + four + 8 * k;  // lanes 4 four .. have the logits
                                     rows_gone &= rows_gone - 1;
-                                    *reinterpret_cast<uint4*>(part + t * 128) = make_uint4(0, 0, 0, 0);
-                                    *reinterpret_cast<uint4*>(more + t * 128) = make_uint4(0, 0, 0, 0);
+                                    uint4* const at[2] = {reinterpret_cast<uint4*>(part + t * 128), reinterpret_cast<uint4*>(more + t * 128)};
+                                    const __nv_bfloat162 none = __floats2bfloat162_rn(0.0f, 0.0f);
+                                    __nv_bfloat162 sum = none;  // 0 x is 0 of what is finite, else NaN
+#pragma unroll
+                                    for (int i = 0; i < 2; ++i) {
+                                        const uint4 v = *at[i];
+                                        sum = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.x), none, sum);
+                                        sum = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.y), none, sum);
+                                        sum = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.z), none, sum);
+                                        sum = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.w), none, sum);
+                                    }
+                                    if (!__any_sync(~0u, !__hbeq2(sum, none))) {
+                                        if (lane >> 2 == four && !(bad >> (warp >> 1) & 1)) lost &= ~(0x33333333u << 2 * k);
+                                        continue;
+                                    }
+                                    *at[0] = make_uint4(0, 0, 0, 0);
+                                    *at[1] = make_uint4(0, 0, 0, 0);
                                 }
                             }
                         }

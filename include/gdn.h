@@ -892,8 +892,10 @@ size_t gdn_latent_attention_workspace_bytes(void);
  *   workspace  as for gdn_kv_attention: zeroed once, one for each of the calls that may overlap;
  *           gdn_kv_attention_status() and gdn_kv_attention_device_status() tell of waits that gave up.
  * out, lse and the workspace share no memory with one another or with what is read.
- * What is not finite in a token's row reaches the outputs of the rows that see it, and of no others; a table entry outside the cache
- * reads as NaN.  What lies in the cache past a request's length is never used.
+ * What is not finite in a token's row reaches the outputs of the rows that see it, and of no others: by its logit (NaN or
+ * inf makes NaN of the row, -inf is a weight of zero), and in the latent part whatever the logit.  A row whose logits are
+ * all -inf gets what one that sees nothing gets.  A table entry outside the cache reads as NaN.  What lies in the cache past a
+ * request's length is never used.
  */
 int gdn_latent_attention(const gdn_latent_shape* shape, int32_t T, const gdn_bf16* q, int64_t q_row, int64_t q_head, const gdn_bf16* q_rope,
                          int64_t r_row, int64_t r_head, const gdn_bf16* cache, const int32_t* table, const int32_t* start,
@@ -911,7 +913,8 @@ int gdn_latent_attention(const gdn_latent_shape* shape, int32_t T, const gdn_bf1
  *   scale, out bf16 [T, H, 128], lse fp32 [T, H] or NULL: as for gdn_latent_attention.
  * out and lse share no memory with one another or with what is read.
  * A query that sees nothing (L < n) gets out = 0, lse = -inf; rows outside start[0] .. start[B] - 1 are not written.  What is
- * not finite in a token's k, k_rope or v reaches the outputs of the queries that see it, and of no others.
+ * not finite in a token's k, k_rope or v reaches the outputs of the queries that see it, and of no others (k and k_rope by the
+ * logit, v whatever the logit, as for gdn_latent_attention).
  * gdn_kv_attention_device_status() tells of waits that gave up.
  */
 int gdn_latent_attention_expanded(int32_t B, int32_t H, int32_t T, int32_t S, const gdn_bf16* q, int64_t q_row, int64_t q_head,
