@@ -42,7 +42,8 @@ struct RotaryParams {
     const uint64_t* turns;      // [rot / 2]
     float factor, eps, inv_d;
     int T, Hq, H;               // H: heads of q and k
-    int chunks, rot_chunks;     // of eight channels: a head's, the rotated ones
+    int touched[2];             // channels of a head of q and of k that are read and written
+    int rot_chunks;             // of eight channels, the rotated ones
     int log2_lanes;             // lanes of a head
     int tokens, heads;          // of a CTA
     int step;                   // from a group's token to its next
@@ -101,8 +102,9 @@ __global__ void __launch_bounds__(kThreads, 3) gdn_rotary_kernel(const __grid_co
     const bool first = 2 * lane < p.rot_chunks, turned = lane < p.rot_chunks;
     int token = group / p.heads;
     const int h = blockIdx.y * p.heads + group % p.heads;
-    const bool have = h < p.H && token < p.step && lane < p.chunks;
-    const int which = h >= p.Hq, hw = min(h, p.H - 1) - (which ? p.Hq : 0);
+    const int which = h >= p.Hq;
+    const bool have = h < p.H && token < p.step && 8 * lane < p.touched[which];
+    const int hw = min(h, p.H - 1) - (which ? p.Hq : 0);
     const int64_t row = p.row[which], out_row = p.out_row[which];
     int64_t from = (t0 + token) * row + hw * p.head[which] + 8 * lane, to = (t0 + token) * out_row + hw * p.out_head[which] + 8 * lane;
     const void* x = p.x[which];
@@ -323,7 +325,7 @@ int gdn_rotary(const gdn_rotary_shape* s, const void* q, int64_t q_row, int64_t 
     const int64_t row[2] = {q_row, k_row}, head[2] = {q_head, k_head}, out_row[2] = {q_out_row, k_out_row}, out_head[2] = {q_out_head, k_out_head};
     const float* norm[2] = {q_norm, k_norm};
     const char *xn[2] = {"q", "k"}, *yn[2] = {"q_out", "k_out"}, *nn[2] = {"q_norm", "k_norm"};
-    bool in_place = true, any_norm = false;
+    int touched[2] = {0, 0};
     for (int i = 0; i < 2; ++i) {
         if (H[i] == 0) continue;
         if ((rc = check_view(x[i], row[i], head[i], s->T, H[i], s->d, size, false, xn[i])) ||
@@ -331,8 +333,7 @@ int gdn_rotary(const gdn_rotary_shape* s, const void* q, int64_t q_row, int64_t 
             (norm[i] != nullptr && (rc = check_pointer(norm[i], nn[i]))))
             return rc;
         const bool same = x[i] == y[i] && (s->T == 1 || row[i] == out_row[i]) && (H[i] == 1 || head[i] == out_head[i]);
-        in_place = in_place && same;
-        any_norm = any_norm || norm[i] != nullptr;
+        touched[i] = same && norm[i] == nullptr ? s->rot : s->d;
         const View out(y[i], out_row[i], out_head[i], s->T, H[i], s->d, size);
         for (int j = 0; j < 2; ++j) {
             if (H[j] == 0) continue;
@@ -352,6 +353,7 @@ int gdn_rotary(const gdn_rotary_shape* s, const void* q, int64_t q_row, int64_t 
         p.head[i] = H[i] > 1 ? head[i] : 0;
         p.out_row[i] = s->T > 1 ? out_row[i] : 0;
         p.out_head[i] = H[i] > 1 ? out_head[i] : 0;
+        p.touched[i] = touched[i];
     }
     p.positions = positions;
     p.turns = turns;
@@ -362,9 +364,8 @@ int gdn_rotary(const gdn_rotary_shape* s, const void* q, int64_t q_row, int64_t 
     p.Hq = s->Hq;
     p.H = s->Hq + s->Hk;
     p.rot_chunks = s->rot / 8;
-    p.chunks = in_place && !any_norm ? p.rot_chunks : s->d / 8;  // what lies past the rotated channels stays where it is
     p.interleaved = (flags & GDN_ROTARY_INTERLEAVED) != 0;
-    while ((1 << p.log2_lanes) < p.chunks) ++p.log2_lanes;
+    while (8 << p.log2_lanes < std::max(touched[0], touched[1])) ++p.log2_lanes;
     // A CTA's groups have a head each, or, where the heads are fewer, several tokens at a time; its tokens are what a group
     // has in flight eight times over, more for few heads, fewer while there are not four CTAs for every SM.
     const int groups = kThreads >> p.log2_lanes;

@@ -826,7 +826,7 @@ typedef struct gdn_rotary_shape {
  *   q, k       bf16 [T, Hq, d], [T, Hk, d] (fp32 with GDN_IN_F32): strides between tokens (row) and heads in
  *              elements, multiples of 16 bytes; slices of a projection's rows, parts of wider heads.
  *   q_out, k_out  the same, with strides of their own: q and k themselves (the same address and strides: in
- *              place; channels past rot are then not touched unless there is a norm), or views that share
+ *              place; its channels past rot are then not touched unless it has a norm), or views that share
  *              no element with them.  Overlap that can be told from the strides is refused.
  *   positions  int32 [T], any sign.   turns  uint64 [rot / 2], device.   factor  finite.
  *   q_norm, k_norm  fp32 [d], or NULL: no norm.   eps in [0, 1].
