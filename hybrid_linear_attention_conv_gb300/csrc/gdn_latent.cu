@@ -16,7 +16,6 @@
 namespace gdn {
 namespace {
 
-__device__ __forceinline__ float bf16f(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
 __device__ __forceinline__ void unpack8(uint4 w, float (&v)[8]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll

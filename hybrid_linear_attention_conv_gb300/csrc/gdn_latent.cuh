@@ -50,7 +50,7 @@ struct LatentAttnParams {
     int64_t q_row, q_head, r_row, r_head;
     int T, B, H, width, pages, log2_page;
     int ctas;                   // of the grid
-    int pair;                   // CTAs that take row tiles of the same tokens, 1 or 2
+    int pair;                   // CTAs that take row tiles of the same tokens: 1 to 2 of 64 rows, 4 of 32, 8 of 16
     float scale_log2;           // scale * log2(e)
 };
 

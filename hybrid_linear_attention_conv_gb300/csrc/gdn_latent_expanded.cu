@@ -14,10 +14,10 @@
 // Their sum is of the unrounded ones, in fp32.
 //
 // Blocks of 256 queries are CTAs of the grid, those with the most tokens first (23 ragged chunks: 193 us with requests in
-// order, 167 so; 149 with what came after).  A CTA that has done one takes over the next that has not begun (cluster launch control), so that
+// order, 167 so; 151 with what came after; requests past kSorted come in their order: 128 of 8 heads 322 us, 129 337).  A CTA that has done one takes over the next that has not begun (cluster launch control), so that
 // a block's queries and first keys are on their way while the one before it ends.
 //
-// Bound by the tensor pipe, in a chain: 8,192 queries and tokens of 32 heads take 525 us, 1.31 PFLOP/s, 3,900 cycles for
+// Bound by the tensor pipe, in a chain: 8,192 queries and tokens of 32 heads take 525 to 545 us (by box), 1.26 to 1.31 PFLOP/s, 3,900 cycles for
 // 256 x 128 of which the products need 2,584.  Few queries after long contexts: by HBM, 4.0 to 4.8 TB/s.
 #include <cuda_bf16.h>
 

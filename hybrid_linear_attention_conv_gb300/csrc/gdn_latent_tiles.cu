@@ -20,9 +20,9 @@
 // weights are rounded to bf16, as the values are: within 2^-8 of themselves, however far below
 // the reference; their sum is of the unrounded ones, in fp32.
 //
-// 64 requests of 4,096 to 12,288 tokens, 128 heads, one token each: 215 us, 663 TFLOP/s, 2.8 TB/s.  A tile of 64 tokens
+// 64 requests of 4,096 to 12,288 tokens, 128 heads, one token each: 217 us, 659 TFLOP/s, 2.8 TB/s.  A tile of 64 tokens
 // and 64 rows takes about 3,100 cycles, 1,950 of them products: bound by shared memory, which serves the MMAs' operands and
-// takes the next tile in.  251 requests of up to 3,000 tokens, 20 heads: 94 us, 4.9 TB/s, HBM and the items' ends.  One
+// takes the next tile in.  251 requests of up to 3,000 tokens, 20 heads: 95 us, 4.8 TB/s, HBM and the items' ends.  One
 // request of 131,072 tokens, 64 heads: 53 us, of which 27 are the first copies, the last output and the join.
 //
 // The list of all (request, row tile, token tile) is cut evenly over the CTAs, one to an SM; an item that
@@ -129,7 +129,7 @@ struct Walk {
             const int v1 = (int)min((long long)kt + kItemCost, v0 + (x1 - x));
             j0 = max(0, v0 - kItemCost);
             j1 = max(0, v1 - kItemCost);
-            // (a pair's second CTA has nothing to do in a group of one row tile)
+            // (a group's last row tiles may have no rows: their CTAs have nothing to do in it)
             if (j0 < j1 && t * list.per_group + side * N < (unsigned)r.n * list.p.H) return true;
             next(v1);
         }
@@ -1015,9 +1015,11 @@ size_t latent_tiles_workspace() { return (size_t)2 * std::min(device_sm_count(),
 // Rows of an item: what the requests have on average, up to 64.  Fewer where the contexts that the table has room for are so
 // short that a CTA gets a few tiles only: an item's queries, products and output are then most of the time, and the rows of
 // one request go to up to eight CTAs that work on the same tokens.  Measured in us at 16, 32 and 64 rows for contexts that
-// give a CTA t tiles of 16 rows: one request of 32 heads, 4,096 tokens (t = 0.9) 16.1, 19.2; 16 of 32 heads, 2,000 (6.7) 20.9,
-// 25.8; 4 of 128 heads, 2,000 (6.7) 22.8, 23.1, 33.9; 4,096 (13.5) 30.4, 29.7, 36.7; 16 of 64 heads, 2,000 (13.5) 27.7, 25.9,
-// 29.0; one of 64 heads, 16,000 (6.6) 21.9, 22.8, 23.8; 40,000 (16) 33.9, 31.0, 29.9; 4 of 64 heads, 16,000 (26) 43.2, 40.6, 37.4.
+// give a CTA t tiles of 16 rows: one request of 32 heads, 4,096 tokens (t = 0.8) 13.0, 15.3; 16 of 32 heads, 2,000 (6.7) 20.8,
+// 20.8; 4 of 128 heads, 2,000 (6.7) 20.6, 21.2, 27.9; 4,096 (13.5) 26.4, 23.8, 31.4; 8 of 64 heads, 1,000 (3.4) 16.2, 17.4, 28.2;
+// 16 of 64 heads, 2,000 (13.5) 27.5, 25.2, 23.9; one of 64 heads, 16,000 (6.6) 19.7, 20.1, 19.2; 40,000 (16) 30.4, 26.6, 24.3;
+// 4 of 64 heads, 16,000 (26) 41.9, 37.2, 32.2.  The host knows the table's width and not the lengths: a table with room
+// for much more than its contexts gets the rows of long ones (the last of three figures, or of two).
 cudaError_t launch_latent_tiles(LatentAttnParams& p, cudaStream_t s) {
     const int64_t rows = ((int64_t)p.T * p.H + p.B - 1) / p.B, sms = device_sm_count();
     const int64_t tiles = (((int64_t)p.width << p.log2_page) + kTok - 1) / kTok;  // of the longest request that the table has room for

@@ -10,8 +10,8 @@
 //
 // Each value is read once and written once.  8,192 tokens of 28 heads of 256, normed, the first 64 channels turned: 47.8 us,
 // 4.9 TB/s, bound by the chain from a token's loads to its stores, of which 24 warps to an SM fill two issue slots of three
-// (with a group's heads and tokens found anew for each, about 300 instructions instead of 90: 74 us).  3,001 tokens of
-// 64 heads of 64, no norm: 7.4 us, 6.6 TB/s, HBM.
+// (with a group's heads and tokens found anew for each, about 300 instructions instead of 90: 74 us).  In fp32 76.6 us,
+// 6.1 TB/s, HBM.  3,001 tokens of 64 heads of 64, no norm: 7.4 us, 6.6 TB/s, HBM.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -870,7 +870,8 @@ typedef struct gdn_latent_shape {
  *   turns, factor  as for gdn_rotary with rot = 64 (uint64 [32], device).
  *   norm       fp32 [512], or NULL: no norm (the latent part is copied).   eps in [0, 1].
  *   flags      GDN_ROTARY_INTERLEAVED.
- * B, H and width of the shape are checked and not used.  fp32 arithmetic, one rounding.
+ * B, H and width of the shape are checked and not used.  fp32 arithmetic, one rounding.  The rows that are written share no memory with
+ * what is read.
  */
 int gdn_latent_append(const gdn_latent_shape* shape, int32_t T, const gdn_bf16* x, int64_t ldx, int32_t n_src, const int32_t* positions,
                       const int64_t* slots, const int32_t* rows, const uint64_t* turns, float factor, const float* norm, float eps,
@@ -887,7 +888,8 @@ size_t gdn_latent_attention_workspace_bytes(void);
  * nothing gets out = 0, lse = -inf.
  *   q       bf16 [T, H, 512], q_rope bf16 [T, H, 64]: strides between tokens (row) and heads in elements, multiples of 8
  *           (a product over the heads leaves q as [H, T, 512]).  Rows outside start[0] .. start[B] - 1 are not written.
- *   table, start, lens  as gdn_kv_plan leaves them (lens after the step).   tree  int64 [T], or NULL (causal).
+ *   table, start, lens  as gdn_kv_plan leaves them (lens after the step); how the work is cut goes by the table's width, and a table no
+ *           wider than the step's longest request is the faster one (up to 1.7 times, for short contexts).   tree  int64 [T], or NULL (causal).
  *   scale   in (0, 1e6].   out  bf16 [T, H, 512], rounded once.   lse  fp32 [T, H], or NULL.
  *   workspace  as for gdn_kv_attention: zeroed once, one for each of the calls that may overlap;
  *           gdn_kv_attention_status() and gdn_kv_attention_device_status() tell of waits that gave up.

@@ -82,7 +82,8 @@ def sentinel():
 
 # blocks of one tile, of two and three, of one and of two tiles of queries, with and without contexts; several to a CTA
 @pytest.mark.parametrize("H,lens,new", [(32, [100] * 40, [100] * 40), (16, [300, 130, 20] * 14, [1, 130, 20] * 14), (24, [256] * 20, [256] * 20),
-                                        (8, [390] * 90, [200] * 90)], ids=str)
+                                        (8, [390] * 90, [200] * 90)],
+                         ids=["one tile", "chunks and single tokens", "two tiles of queries", "after contexts"])
 def test_expanded_writes_nothing_outside(H, lens, new):
     c = expanded_case(22, H, lens, new)
     T, S, first = sum(new), sum(lens), 5
@@ -98,7 +99,8 @@ def test_expanded_writes_nothing_outside(H, lens, new):
     under_limits(call, inside, want, sentinel())
 
 
-@pytest.mark.parametrize("H,lens,new", [(160, [3000], [100]), (152, [128 * 5], [128]), (32, [2000] * 5, [3] * 5)], ids=str)
+@pytest.mark.parametrize("H,lens,new", [(160, [3000], [100]), (152, [128 * 5], [128]), (32, [2000] * 5, [3] * 5)],
+                         ids=["joined", "five tiles", "few queries"])
 def test_expanded_last_blocks_copies_land(H, lens, new):
     """A block or two to a CTA, whose loader is through with its copies long before they are used: a wait that gives up then
     must not end the CTA before they have landed (in what may be another's shared memory by then)."""
@@ -116,7 +118,8 @@ def test_expanded_last_blocks_copies_land(H, lens, new):
 
 # items of 16, 32 and 64 rows, several to a CTA, of one tile and of many, whole and in parts; causal and by tree
 @pytest.mark.parametrize("H,lens,new", [(8, [100] * 700, [1] * 700), (64, [200, 30] * 60, [1, 2] * 60), (128, [700] * 30, [1] * 30),
-                                        (20, [3000, 64, 500] * 20, [1, 1, 3] * 20), (64, [300] * 8, [40] * 8)], ids=str)
+                                        (20, [3000, 64, 500] * 20, [1, 1, 3] * 20), (64, [300] * 8, [40] * 8)],
+                         ids=["many short", "64 rows", "pairs", "parts", "chunks"])
 def test_absorbed_ends_and_writes_nothing_outside(H, lens, new):
     c = latent_case(24, H, 64, lens, new)
     T, first = sum(new), 3
